@@ -432,6 +432,166 @@ qsa_status_t qsa_mqa_paged_batch(const void* q, int64_t q_stride_t, int64_t q_st
 size_t qsa_mqa_paged_batch_workspace_size(int32_t R, int32_t num_decodes, int32_t decode_query_len, int64_t T,
                                           int32_t W);
 
+/*
+ * The 8-bit K/V cache of the core attention.
+ *
+ * Codes are E4M3 (as in qsa_mqa_decode_fp8: largest finite 448, NaN 0x7f /
+ * 0xff), with one fp32 scale per block of block_tokens consecutive tokens of
+ * a page and KV head: element c of token row r of page p and head g stands for
+ *     E4M3(code) * scale[p, r / block_tokens, g].
+ *   k_cache,   codes [num_pages, page_size, Hkv, 256], page, row and head
+ *   v_cache    strides in BYTES (positive multiples of 16, at least 256);
+ *              16-byte aligned; the same strides for K and V.  Rows outermost
+ *              or heads outermost inside a page, and K and V interleaved in
+ *              one pool, are all strides.
+ *   k_scale,   fp32 [num_pages, page_size / block_tokens, Hkv]: page and
+ *   v_scale    block strides in elements, unit head stride; > 0 and finite
+ *              for every block that holds a token.
+ *   block_tokens  1 .. page_size, dividing page_size (any page_size >= 1).
+ * The pages' K/V cache is 16-bit; this one halves its memory and traffic.
+ * Requests, rows and page tables are those of qsa_sparse_attention: row i of
+ * request r sits at logical position seq_lens[r] - qlen_r + i, entries of
+ * page_table outside [0, num_pages) are missing pages.  Rows at or behind
+ * cu_seqlens_q[R] (a padded batch) belong to no request.
+ */
+
+/*
+ * qsa_kv_append_fp8 - quantise new K and V rows into the cache.
+ *
+ * Row i of request r is written at its logical position.  For every scale
+ * block that gets rows, with A the largest finite magnitude among them:
+ *     need = the smallest power of two s >= 2^-64 with A <= 448 s
+ *     s'   = need                  if the block's first token is among them
+ *          = max(s, need)          otherwise (s: the block's scale so far)
+ * New elements become E4M3(x / s') (nearest even; NaN stays NaN, infinities
+ * become +-448).  If s' != s the block's tokens in front of the first new row
+ * become E4M3(E4M3 value * s / s').  Tokens behind the last new row are left
+ * as they are: they are not part of the request any more (rejected
+ * speculative tokens are overwritten this way).  Rows whose page is missing or
+ * whose position is negative are dropped; nothing else in the caches or scales
+ * changes.  Two requests must not write to the same page.
+ *   k, v       bf16 [T, Hkv, 256], each with its own row and head strides
+ *              (positive multiples of 8 elements); 16-byte aligned; must not
+ *              overlap the caches.
+ *   token_weight  int64 [num_pages, page_size] contiguous, or NULL: set to 0
+ *              for the tokens written (see qsa_accumulate_weights).
+ * One launch.
+ */
+qsa_status_t qsa_kv_append_fp8(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+                               int64_t v_stride_t, int64_t v_stride_h, void* k_cache, void* v_cache, float* k_scale,
+                               float* v_scale, int64_t num_pages, int32_t page_size, int32_t block_tokens,
+                               int64_t kv_page_stride, int64_t kv_row_stride, int64_t kv_head_stride,
+                               int64_t scale_page_stride, int64_t scale_block_stride, int32_t Hkv,
+                               const int32_t* page_table, int64_t pt_stride, int32_t max_pages,
+                               const int32_t* cu_seqlens_q, const int32_t* seq_lens, int32_t R, int64_t T,
+                               int64_t* token_weight, void* stream);
+
+/* qsa_kv_append_fp8_f16 - the same for fp16 rows. */
+qsa_status_t qsa_kv_append_fp8_f16(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+                                   int64_t v_stride_t, int64_t v_stride_h, void* k_cache, void* v_cache,
+                                   float* k_scale, float* v_scale, int64_t num_pages, int32_t page_size,
+                                   int32_t block_tokens, int64_t kv_page_stride, int64_t kv_row_stride,
+                                   int64_t kv_head_stride, int64_t scale_page_stride, int64_t scale_block_stride,
+                                   int32_t Hkv, const int32_t* page_table, int64_t pt_stride, int32_t max_pages,
+                                   const int32_t* cu_seqlens_q, const int32_t* seq_lens, int32_t R, int64_t T,
+                                   int64_t* token_weight, void* stream);
+
+/*
+ * qsa_sparse_attention_fp8 - qsa_sparse_attention over the 8-bit cache: the
+ * same definition on the keys and values that the codes and scales stand for.
+ *
+ * Codes enter the tensor cores as they are; queries and probabilities are
+ * split into E4M3 terms (a bf16 query element exactly, a probability to 2^-12
+ * relative), all sums are fp32.
+ *   weights    fp32 [T, width], row stride weights_stride (>= width), or
+ *              NULL: weights[t, e] = sum over the Hq query heads of entry e's
+ *              softmax probability, 0 for entries that the row does not see.
+ *   workspace  16-byte aligned, qsa_sparse_attention_fp8_workspace_size(T,
+ *              Hq, Hkv, width, weights != NULL) bytes; its contents do not
+ *              matter before or after.
+ * Other arguments, empty rows and errors as qsa_sparse_attention.  A query
+ * head with a NaN or infinite element gives NaN.
+ */
+qsa_status_t qsa_sparse_attention_fp8(const void* q, int64_t q_stride_t, int64_t q_stride_h, int32_t Hq,
+                                      const void* k_cache, const void* v_cache, const float* k_scale,
+                                      const float* v_scale, int64_t num_pages, int32_t page_size,
+                                      int32_t block_tokens, int64_t kv_page_stride, int64_t kv_row_stride,
+                                      int64_t kv_head_stride, int64_t scale_page_stride, int64_t scale_block_stride,
+                                      int32_t Hkv, const int32_t* page_table, int64_t pt_stride, int32_t max_pages,
+                                      const int32_t* cu_seqlens_q, const int32_t* seq_lens, int32_t R,
+                                      const int32_t* token_idx, int64_t tok_stride, int32_t width, int64_t T,
+                                      const float* gate, float scale, void* out, int64_t out_stride_t, float* lse,
+                                      float* weights, int64_t weights_stride, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* qsa_sparse_attention_fp8_f16 - the same for fp16 q and out. */
+qsa_status_t qsa_sparse_attention_fp8_f16(const void* q, int64_t q_stride_t, int64_t q_stride_h, int32_t Hq,
+                                          const void* k_cache, const void* v_cache, const float* k_scale,
+                                          const float* v_scale, int64_t num_pages, int32_t page_size,
+                                          int32_t block_tokens, int64_t kv_page_stride, int64_t kv_row_stride,
+                                          int64_t kv_head_stride, int64_t scale_page_stride,
+                                          int64_t scale_block_stride, int32_t Hkv, const int32_t* page_table,
+                                          int64_t pt_stride, int32_t max_pages, const int32_t* cu_seqlens_q,
+                                          const int32_t* seq_lens, int32_t R, const int32_t* token_idx,
+                                          int64_t tok_stride, int32_t width, int64_t T, const float* gate,
+                                          float scale, void* out, int64_t out_stride_t, float* lse, float* weights,
+                                          int64_t weights_stride, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/* 0 when there is nothing to compute (T, Hq, Hkv or width <= 0). */
+size_t qsa_sparse_attention_fp8_workspace_size(int64_t T, int32_t Hq, int32_t Hkv, int32_t width, int32_t weights);
+
+/*
+ * qsa_accumulate_weights - add attention weights up per cached token.
+ *
+ * token_weight counts in units of 2^-32: for every entry e of row t that the
+ * row sees (0 <= j <= pos, j < seq_lens[r], valid page),
+ *     token_weight[page, j % page_size] += rint(min(weights[t, e], 2^20) * 2^32)
+ * (ties to even); weights that are NaN or not positive add nothing.  The sums
+ * are integers, so neither the order of the additions nor tokens listed twice
+ * or shared by requests make a result depend on the run.
+ *   weights    fp32 [T, width], row stride weights_stride; token_idx int32
+ *              [T, width], row stride tok_stride.
+ *   token_weight  int64 [num_pages, page_size] contiguous, 8-byte aligned;
+ *              must not overlap the inputs.  The caller zeroes it once;
+ *              qsa_kv_append_fp8 zeroes what it writes.
+ * One launch.
+ */
+qsa_status_t qsa_accumulate_weights(const float* weights, int64_t weights_stride, const int32_t* token_idx,
+                                    int64_t tok_stride, int32_t width, int64_t T, const int32_t* page_table,
+                                    int64_t pt_stride, int32_t max_pages, const int32_t* cu_seqlens_q,
+                                    const int32_t* seq_lens, int32_t R, int64_t* token_weight, int64_t num_pages,
+                                    int32_t page_size, void* stream);
+
+/*
+ * qsa_evict_pages - drop each request's pages of least accumulated weight.
+ *
+ * Request r's logical pages are 0 .. ceil(seq_lens[r] / page_size) - 1 (at
+ * most max_pages); those with a valid entry are live.  The first keep_first
+ * and the last keep_last logical pages are never dropped.  Of the other live
+ * pages the heaviest stay, as many as keep[r] leaves after the live pages
+ * just named, the earlier page among equals; the rest are dropped.  A page's
+ * weight is the (64-bit integer) sum of its page_size token weights.
+ *   table_out  int32 [R, max_pages]: page_table with -1 for dropped pages;
+ *              may be page_table itself (same stride).
+ *   freed      int32 [R, max_pages]: the dropped entries in page order, then
+ *              -1.  counts int32 [R]: how many.
+ * Attention and indexer calls mask tokens and keys of missing pages, so the
+ * new table can be used as it is; positions do not change.  A compressed key
+ * cache of page_size / 4 rows per page can share the table.  A page that
+ * several requests share is dropped for each on its own: the caller counts
+ * references.  keep, seq_lens: int32 [R].
+ *   workspace  16-byte aligned, qsa_evict_pages_workspace_size(R, max_pages)
+ *              bytes.
+ */
+qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int32_t page_size,
+                             const int32_t* page_table, int64_t pt_stride, int32_t max_pages, const int32_t* seq_lens,
+                             const int32_t* keep, int32_t R, int32_t keep_first, int32_t keep_last, int32_t* table_out,
+                             int64_t out_stride, int32_t* freed, int64_t freed_stride, int32_t* counts,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+size_t qsa_evict_pages_workspace_size(int32_t R, int32_t max_pages);
+
 #ifdef __cplusplus
 }
 #endif

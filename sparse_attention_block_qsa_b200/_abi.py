@@ -19,6 +19,11 @@ SCALE = 1.0 / math.sqrt(128.0)
 
 _i64, _i32, _f32, _vp, _sz = C.c_int64, C.c_int32, C.c_float, C.c_void_p, C.c_size_t
 
+# the 8-bit cache: codes, scales and their strides, then the page table
+_CACHE8 = [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _i32]
+_APPEND = [_vp, _i64, _i64, _vp, _i64, _i64, *_CACHE8, _i64, _vp, _vp]
+_ATTN8 = [_vp, _i64, _i64, _i32, *_CACHE8, _vp, _i64, _i32, _i64, _vp, _f32, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp]
+
 SIGNATURES = {
     "qsa_status_string": (C.c_char_p, [C.c_int]),
     "qsa_last_error_detail": (C.c_char_p, []),
@@ -51,6 +56,16 @@ SIGNATURES = {
     "qsa_mqa_paged_batch": (C.c_int, [_vp, _i64, _i64, _vp, _i64, _i32, _i64, _i64, _vp, _i64, _i32, _vp, _vp,
                                       _i32, _i32, _i32, _i64, _f32, _vp, _i64, _i32, _vp, _sz, _vp]),
     "qsa_mqa_paged_batch_workspace_size": (_sz, [_i32, _i32, _i32, _i64, _i32]),
+    "qsa_kv_append_fp8": (C.c_int, _APPEND),
+    "qsa_kv_append_fp8_f16": (C.c_int, _APPEND),
+    "qsa_sparse_attention_fp8": (C.c_int, _ATTN8),
+    "qsa_sparse_attention_fp8_f16": (C.c_int, _ATTN8),
+    "qsa_sparse_attention_fp8_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "qsa_accumulate_weights": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _vp,
+                                         _i64, _i32, _vp]),
+    "qsa_evict_pages": (C.c_int, [_vp, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i64, _vp,
+                                  _i64, _vp, _vp, _sz, _vp]),
+    "qsa_evict_pages_workspace_size": (_sz, [_i32, _i32]),
 }
 
 STATUS = {0: "QSA_OK", 1: "QSA_ERR_INVALID_ARG", 2: "QSA_ERR_ALIGNMENT", 3: "QSA_ERR_UNSUPPORTED",
@@ -422,3 +437,222 @@ def mqa_paged_batch(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Te
         _ptr(seq_lens), R, num_decodes, decode_query_len, T, scale, _ptr(out), out.stride(0), W,
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
+
+
+def _placed(stream, *tensors):
+    """(device, stream handle) of a call on the given tensors (None skipped): they must all live on one device, and
+    the call runs there, on `stream` or on that device's current stream."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one call needs one device")
+    if stream is None:
+        return dev, C.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return dev, _stream(stream)
+
+
+def _new(stream, shape, dtype, dev):
+    """Memory that belongs to the stream the call runs on (an output or a workspace made here)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _call(dev, name, *args):
+    """The library call with `dev` current."""
+    if dev.index == torch.cuda.current_device():
+        _check(name, getattr(lib(), name)(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, getattr(lib(), name)(*args))
+
+
+def _workspace(workspace, need, stream, dev):
+    if workspace is None:
+        workspace = _new(stream, (max(need, 16),), torch.uint8, dev)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _cache8(k_cache, v_cache, k_scale, v_scale):
+    """Check the 8-bit cache's tensors; returns (codes of K, codes of V, block_tokens)."""
+    k_cache, v_cache = (c.view(torch.uint8) if isinstance(c, torch.Tensor) and c.dtype == torch.float8_e4m3fn else c
+                        for c in (k_cache, v_cache))
+    _need(k_cache, "k_cache", torch.uint8, 4)
+    _need(v_cache, "v_cache", torch.uint8, 4)
+    _need(k_scale, "k_scale", torch.float32, 3)
+    _need(v_scale, "v_scale", torch.float32, 3)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.shape[3] != 256 \
+            or k_cache.stride(3) != 1:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, 256] with the same strides")
+    pages, ps, Hkv, _ = k_cache.shape
+    blocks = k_scale.shape[1]
+    if k_scale.shape != v_scale.shape or k_scale.stride() != v_scale.stride() or k_scale.stride(2) != 1 \
+            or k_scale.shape[0] != pages or k_scale.shape[2] != Hkv or blocks < 1 or ps % blocks:
+        raise ValueError("k_scale and v_scale must be [pages, blocks, Hkv] with the same strides, unit head stride, "
+                         "and blocks must divide page_size")
+    return k_cache, v_cache, ps // blocks
+
+
+def _tables(page_table, cu_seqlens_q, seq_lens):
+    _need(page_table, "page_table", torch.int32, 2)
+    _index_checks(cu_seqlens_q, seq_lens)
+    if page_table.stride(1) != 1 or page_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("page_table needs one row per request and a unit column stride")
+
+
+def _token_weight(token_weight, pages, page_size):
+    _need(token_weight, "token_weight", torch.int64, 2)
+    if token_weight.shape != (pages, page_size) or not token_weight.is_contiguous():
+        raise ValueError("token_weight must be contiguous int64 [pages, page_size]")
+
+
+def kv_append_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  k_scale: torch.Tensor, v_scale: torch.Tensor, page_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                  seq_lens: torch.Tensor, token_weight: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise new rows k, v (bf16 or fp16 [T, Hkv, 256]) into the 8-bit cache, in place: k_cache, v_cache
+    float8_e4m3fn (or uint8 codes) [pages, page_size, Hkv, 256], k_scale, v_scale fp32 [pages, page_size /
+    block_tokens, Hkv].  Row i of request r goes to position seq_lens[r] - qlen_r + i.  A block's scale is the
+    smallest power of two that holds it; it grows when a later token needs it.  token_weight (int64 [pages,
+    page_size]) is zeroed for the tokens written."""
+    dt = k.dtype if isinstance(k, torch.Tensor) and k.dtype == torch.float16 else torch.bfloat16
+    _need(k, "k", dt, 3)
+    _need(v, "v", dt, 3)
+    k_cache, v_cache, bt = _cache8(k_cache, v_cache, k_scale, v_scale)
+    _tables(page_table, cu_seqlens_q, seq_lens)
+    pages, ps, Hkv, _ = k_cache.shape
+    if k.shape != v.shape or k.shape[1:] != (Hkv, 256) or k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v must be [T, Hkv, 256] with unit feature stride")
+    if token_weight is not None:
+        _token_weight(token_weight, pages, ps)
+    dev, st = _placed(stream, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seq_lens,
+                      token_weight)
+    _call(dev, "qsa_kv_append_fp8_f16" if dt == torch.float16 else "qsa_kv_append_fp8",
+          _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _ptr(k_cache), _ptr(v_cache),
+          _ptr(k_scale), _ptr(v_scale), pages, ps, bt, k_cache.stride(0), k_cache.stride(1), k_cache.stride(2),
+          k_scale.stride(0), k_scale.stride(1), Hkv, _ptr(page_table), page_table.stride(0), page_table.shape[1],
+          _ptr(cu_seqlens_q), _ptr(seq_lens), seq_lens.shape[0], k.shape[0], _ptr(token_weight), st)
+
+
+def sparse_attention_fp8_workspace_size(T: int, Hq: int, Hkv: int, width: int, weights: bool = False) -> int:
+    return int(lib().qsa_sparse_attention_fp8_workspace_size(T, Hq, Hkv, width, 1 if weights else 0))
+
+
+def sparse_attention_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                         v_scale: torch.Tensor, page_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                         seq_lens: torch.Tensor, token_idx: torch.Tensor, scale: float,
+                         gate: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None):
+    """sparse_attention over the 8-bit cache of kv_append_fp8: q bf16 or fp16 [T, Hq, 256] -> (out of q's type
+    [T, Hq, 256], lse fp32 [T, Hq]).  weights (fp32 [T, width]), if given, receives every entry's softmax
+    probability summed over the query heads.  The workspace (any CUDA tensor, 16-byte aligned) is allocated here by
+    torch when not given."""
+    dt = q.dtype if isinstance(q, torch.Tensor) and q.dtype == torch.float16 else torch.bfloat16
+    _need(q, "q", dt, 3)
+    k_cache, v_cache, bt = _cache8(k_cache, v_cache, k_scale, v_scale)
+    _tables(page_table, cu_seqlens_q, seq_lens)
+    _need(token_idx, "token_idx", torch.int32, 2)
+    T, Hq, Dq = q.shape
+    pages, ps, Hkv, _ = k_cache.shape
+    width = token_idx.shape[1]
+    if Dq != 256 or q.stride(2) != 1:
+        raise ValueError("q must be [T, Hq, 256] with unit feature stride")
+    if token_idx.shape[0] != T or token_idx.stride(1) != 1:
+        raise ValueError("token_idx must be [T, width] with unit column stride")
+    if gate is not None:
+        _need(gate, "gate", torch.float32, 2)
+        if gate.shape != (T, Hq) or not gate.is_contiguous():
+            raise ValueError("gate must be contiguous fp32 [T, Hq]")
+    if weights is not None:
+        _need(weights, "weights", torch.float32, 2)
+        if weights.shape != (T, width) or weights.stride(1) != 1:
+            raise ValueError("weights must be fp32 [T, width] with unit column stride")
+    dev, st = _placed(stream, q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seq_lens, token_idx,
+                      gate, out, lse, weights, workspace)
+    if out is None:
+        out = _new(stream, (T, Hq, 256), dt, dev)
+    _need(out, "out", dt, 3)
+    if out.shape != (T, Hq, 256) or out.stride(2) != 1 or out.stride(1) != 256:
+        raise ValueError("out must be [T, Hq, 256] with contiguous heads")
+    if lse is None:
+        lse = _new(stream, (T, Hq), torch.float32, dev)
+    _need(lse, "lse", torch.float32, 2)
+    if lse.shape != (T, Hq) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [T, Hq]")
+    workspace, nbytes = _workspace(
+        workspace, sparse_attention_fp8_workspace_size(T, Hq, Hkv, max(width, 1), weights is not None), stream, dev)
+    _call(dev, "qsa_sparse_attention_fp8_f16" if dt == torch.float16 else "qsa_sparse_attention_fp8",
+          _ptr(q), q.stride(0), q.stride(1), Hq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages, ps,
+          bt, k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), k_scale.stride(0), k_scale.stride(1), Hkv,
+          _ptr(page_table), page_table.stride(0), page_table.shape[1], _ptr(cu_seqlens_q), _ptr(seq_lens),
+          seq_lens.shape[0], _ptr(token_idx), token_idx.stride(0), width, T, _ptr(gate), float(scale), _ptr(out),
+          out.stride(0), _ptr(lse), _ptr(weights), weights.stride(0) if weights is not None else 0, _ptr(workspace),
+          nbytes, st)
+    return out, lse
+
+
+def accumulate_weights(weights: torch.Tensor, token_idx: torch.Tensor, page_table: torch.Tensor,
+                       cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor, token_weight: torch.Tensor,
+                       stream=None) -> torch.Tensor:
+    """Add attention weights (fp32 [T, width], one per entry of token_idx int32 [T, width]) up per cached token, in
+    place: token_weight int64 [pages, page_size] in units of 2^-32.  Returns token_weight."""
+    _need(weights, "weights", torch.float32, 2)
+    _need(token_idx, "token_idx", torch.int32, 2)
+    _need(token_weight, "token_weight", torch.int64, 2)
+    _tables(page_table, cu_seqlens_q, seq_lens)
+    pages, ps = token_weight.shape
+    _token_weight(token_weight, pages, ps)
+    T, width = token_idx.shape
+    if weights.shape != (T, width) or weights.stride(1) != 1 or token_idx.stride(1) != 1:
+        raise ValueError("weights and token_idx must be [T, width] with unit column strides")
+    dev, st = _placed(stream, weights, token_idx, page_table, cu_seqlens_q, seq_lens, token_weight)
+    _call(dev, "qsa_accumulate_weights", _ptr(weights), weights.stride(0), _ptr(token_idx), token_idx.stride(0), width,
+          T, _ptr(page_table), page_table.stride(0), page_table.shape[1], _ptr(cu_seqlens_q), _ptr(seq_lens),
+          seq_lens.shape[0], _ptr(token_weight), pages, ps, st)
+    return token_weight
+
+
+def evict_pages_workspace_size(R: int, max_pages: int) -> int:
+    return int(lib().qsa_evict_pages_workspace_size(R, max_pages))
+
+
+def evict_pages(token_weight: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, keep: torch.Tensor,
+                keep_first: int = 0, keep_last: int = 1, table_out: torch.Tensor | None = None,
+                freed: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """Drop the pages of least accumulated weight (token_weight int64 [pages, page_size]) until request r has
+    keep[r] (int32 [R]) live pages; its first keep_first and last keep_last logical pages stay.  Returns (table_out
+    int32 [R, max_pages] with -1 for dropped pages, freed int32 [R, max_pages]: the dropped pages in order, then -1,
+    counts int32 [R]).  table_out may be page_table."""
+    _need(token_weight, "token_weight", torch.int64, 2)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(keep, "keep", torch.int32, 1)
+    pages, ps = token_weight.shape
+    _token_weight(token_weight, pages, ps)
+    R, max_pages = page_table.shape
+    if seq_lens.shape[0] != R or keep.shape[0] != R or not seq_lens.is_contiguous() or not keep.is_contiguous() \
+            or page_table.stride(1) != 1:
+        raise ValueError("page_table needs one row per request and a unit column stride, seq_lens and keep one "
+                         "contiguous entry per request")
+    dev, st = _placed(stream, token_weight, page_table, seq_lens, keep, table_out, freed, counts, workspace)
+    table_out = _new(stream, (R, max_pages), torch.int32, dev) if table_out is None else table_out
+    freed = _new(stream, (R, max_pages), torch.int32, dev) if freed is None else freed
+    counts = _new(stream, (R,), torch.int32, dev) if counts is None else counts
+    for t, n in ((table_out, "table_out"), (freed, "freed")):
+        _need(t, n, torch.int32, 2)
+        if t.shape != (R, max_pages) or t.stride(1) != 1:
+            raise ValueError(f"{n} must be int32 [R, max_pages] with unit column stride")
+    _need(counts, "counts", torch.int32, 1)
+    if counts.shape[0] != R or not counts.is_contiguous():
+        raise ValueError("counts must be contiguous int32 [R]")
+    workspace, nbytes = _workspace(workspace, evict_pages_workspace_size(R, max_pages), stream, dev)
+    _call(dev, "qsa_evict_pages", _ptr(token_weight), pages, ps, _ptr(page_table), page_table.stride(0), max_pages,
+          _ptr(seq_lens), _ptr(keep), R, int(keep_first), int(keep_last), _ptr(table_out), table_out.stride(0),
+          _ptr(freed), freed.stride(0), _ptr(counts), _ptr(workspace), nbytes, st)
+    return table_out, freed, counts

@@ -18,6 +18,8 @@
 #include "topk.cuh"
 #include "attention.cuh"
 #include "paged_batch.cuh"
+#include "attention_fp8.cuh"
+#include "kv8.cuh"
 
 namespace {
 
@@ -143,6 +145,8 @@ qsa_status_t device_info(int* sms) {
         {reinterpret_cast<const void*>(qsa::prefill::prefill_kernel<false>), qsa::prefill::SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::prefill::prefill_kernel<true>), qsa::prefill::SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::attn::attn_kernel), qsa::attn::SMEM_BYTES},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false>), qsa::attn8::smem_bytes<2>()},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true>), qsa::attn8::smem_bytes<3>()},
         {reinterpret_cast<const void*>(qsa::topk::topk_rows_kernel), qsa::topk::ROWS_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_pipe_kernel), qsa::topk::PIPE_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_filter_kernel), qsa::topk::TP_SMEM_BYTES},
@@ -423,6 +427,74 @@ void attn_splits(int64_t T, int32_t Hkv, int32_t width, int32_t* splits, int32_t
   sp = (chunks + per - 1) / per;
   *splits = (int32_t)sp;
   *cps = (int32_t)per;
+}
+
+// The same for the 8-bit cache's attention: 128-entry tiles, two CTAs per SM.
+void attn8_splits(int64_t T, int32_t Hkv, int32_t width, int32_t* splits, int32_t* tps) {
+  const int64_t tiles = std::max<int64_t>(1, ((int64_t)width + qsa::attn8::TILE - 1) / qsa::attn8::TILE);
+  const int64_t pairs = std::max<int64_t>(1, T * Hkv);
+  int64_t sp = std::min<int64_t>(tiles, std::max<int64_t>(1, 296 / pairs));
+  const int64_t per = (tiles + sp - 1) / sp;
+  sp = (tiles + per - 1) / per;
+  *splits = (int32_t)sp;
+  *tps = (int32_t)per;
+}
+
+// Workspace of the 8-bit cache's attention (bytes from its start).
+struct Attn8Layout {
+  size_t ml, lse2, s, total;
+};
+
+Attn8Layout attn8_layout(int64_t T, int32_t Hq, int32_t Hkv, int32_t width, bool weights) {
+  int32_t splits = 0, tps = 0;
+  attn8_splits(T, Hkv, width, &splits, &tps);
+  const size_t heads = (size_t)T * (size_t)Hq;
+  Attn8Layout w;
+  w.ml = heads * splits * qsa::attn8::D * sizeof(float);
+  w.lse2 = w.ml + heads * splits * 2 * sizeof(float);
+  w.s = w.lse2 + (weights ? heads * sizeof(float) : 0);
+  w.total = w.s + (weights ? heads * (size_t)width * sizeof(float) : 0);
+  return w;
+}
+
+// Checks shared by the calls on an 8-bit K/V cache.
+qsa_status_t check_kv8(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                       int64_t num_pages, int32_t page_size, int32_t block_tokens, int64_t kv_page_stride,
+                       int64_t kv_row_stride, int64_t kv_head_stride, int64_t sc_page_stride, int64_t sc_block_stride,
+                       int32_t Hkv) {
+  constexpr int D = qsa::attn8::D;
+  if (!k_cache || !v_cache || !k_scale || !v_scale) return fail(QSA_ERR_INVALID_ARG, "null cache or scale pointer");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return fail(QSA_ERR_ALIGNMENT, "k_cache and v_cache must be 16-byte aligned");
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return fail(QSA_ERR_ALIGNMENT, "k_scale and v_scale must be 4-byte aligned");
+  const int64_t strides[3] = {num_pages > 1 ? kv_page_stride : 16, page_size > 1 ? kv_row_stride : 16,
+                              Hkv > 1 ? kv_head_stride : 16};
+  for (int64_t st : strides)
+    if (st <= 0 || st % 16 != 0)
+      return fail(QSA_ERR_ALIGNMENT, "cache strides must be positive multiples of 16 bytes (got %lld)", (long long)st);
+  if (Hkv > 1 && kv_head_stride < D) return fail(QSA_ERR_INVALID_ARG, "kv_head_stride below 256 bytes");
+  if (page_size > 1 && kv_row_stride < D) return fail(QSA_ERR_INVALID_ARG, "kv_row_stride below 256 bytes");
+  if (num_pages > 1 && kv_page_stride < D) return fail(QSA_ERR_INVALID_ARG, "kv_page_stride below 256 bytes");
+  const int32_t blocks = page_size / block_tokens;
+  if (blocks > 1 && sc_block_stride < Hkv) return fail(QSA_ERR_INVALID_ARG, "scale block stride below Hkv");
+  if (num_pages > 1 && sc_page_stride < (blocks > 1 ? 1 : Hkv))
+    return fail(QSA_ERR_INVALID_ARG, "scale page stride too small");
+  return QSA_OK;
+}
+
+// Sizes that every call on an 8-bit K/V cache checks first.
+qsa_status_t check_kv8_sizes(int64_t T, int32_t R, int64_t num_pages, int32_t page_size, int32_t block_tokens,
+                             int32_t Hkv, int32_t max_pages) {
+  if (T < 0 || R < 0 || max_pages < 0) return fail(QSA_ERR_INVALID_ARG, "negative size argument");
+  if (num_pages < 1 || num_pages > INT32_MAX) return fail(QSA_ERR_INVALID_ARG, "num_pages out of range");
+  if (page_size < 1) return fail(QSA_ERR_INVALID_ARG, "page_size must be positive");
+  if (block_tokens < 1 || page_size % block_tokens != 0)
+    return fail(QSA_ERR_INVALID_ARG, "block_tokens = %d must divide page_size = %d", block_tokens, page_size);
+  if (Hkv < 1 || Hkv > 65535) return fail(QSA_ERR_UNSUPPORTED, "Hkv = %d out of range", Hkv);
+  if (T > INT32_MAX) return fail(QSA_ERR_UNSUPPORTED, "T = %lld rows exceeds 2^31 - 1", (long long)T);
+  if (T > 0 && R == 0) return fail(QSA_ERR_INVALID_ARG, "T > 0 rows need at least one request");
+  return QSA_OK;
 }
 
 }  // namespace
@@ -1077,6 +1149,353 @@ qsa_status_t qsa_mqa_paged_batch(const void* q, int64_t q_stride_t, int64_t q_st
   // 4. keys whose page is missing
   launch_pdl(qsa::batch::fixup_kernel, dim3(R - D), dim3(qsa::batch::THREADS), 0, s, bp);
   return launch_status("paged-batch fix-up kernel");
+}
+
+static qsa_status_t append_common(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+                                  int64_t v_stride_t, int64_t v_stride_h, void* k_cache, void* v_cache, float* k_scale,
+                                  float* v_scale, int64_t num_pages, int32_t page_size, int32_t block_tokens,
+                                  int64_t kv_page_stride, int64_t kv_row_stride, int64_t kv_head_stride,
+                                  int64_t sc_page_stride, int64_t sc_block_stride, int32_t Hkv,
+                                  const int32_t* page_table, int64_t pt_stride, int32_t max_pages,
+                                  const int32_t* cu_seqlens_q, const int32_t* seq_lens, int32_t R, int64_t T,
+                                  int64_t* token_weight, void* stream, bool f16) {
+  using qsa::kv8::D;
+  qsa_status_t st = check_kv8_sizes(T, R, num_pages, page_size, block_tokens, Hkv, max_pages);
+  if (st != QSA_OK) return st;
+  if (T == 0) return ok();
+  if (!k || !v || !cu_seqlens_q || !seq_lens || (max_pages > 0 && !page_table))
+    return fail(QSA_ERR_INVALID_ARG, "null pointer argument");
+  st = check_kv8(k_cache, v_cache, k_scale, v_scale, num_pages, page_size, block_tokens, kv_page_stride, kv_row_stride,
+                 kv_head_stride, sc_page_stride, sc_block_stride, Hkv);
+  if (st != QSA_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(QSA_ERR_ALIGNMENT, "k and v must be 16-byte aligned");
+  if (!aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) || (page_table && !aligned(page_table, 4)) ||
+      (token_weight && !aligned(token_weight, 8)))
+    return fail(QSA_ERR_ALIGNMENT, "index arrays must be 4-byte and token_weight 8-byte aligned");
+  const int64_t strides[4] = {T > 1 ? k_stride_t : 8, Hkv > 1 ? k_stride_h : 8, T > 1 ? v_stride_t : 8,
+                              Hkv > 1 ? v_stride_h : 8};
+  for (int64_t s : strides)
+    if (s <= 0 || s % 8 != 0)
+      return fail(QSA_ERR_ALIGNMENT, "strides of k and v must be positive multiples of 8 elements (got %lld)", (long long)s);
+  if (max_pages > 0 && R > 1 && pt_stride < max_pages) return fail(QSA_ERR_INVALID_ARG, "pt_stride below max_pages");
+  {
+    const Range in[2] = {span(k, 2, T, T > 1 ? k_stride_t : 0, Hkv, Hkv > 1 ? k_stride_h : 0, 1, 0, D),
+                         span(v, 2, T, T > 1 ? v_stride_t : 0, Hkv, Hkv > 1 ? v_stride_h : 0, 1, 0, D)};
+    for (const void* c : {k_cache, v_cache}) {
+      const Range rc = span(c, 1, num_pages, num_pages > 1 ? kv_page_stride : 0, page_size,
+                            page_size > 1 ? kv_row_stride : 0, Hkv, Hkv > 1 ? kv_head_stride : 0, D);
+      if (overlaps(rc, in[0]) || overlaps(rc, in[1])) return fail(QSA_ERR_INVALID_ARG, "a cache overlaps k or v");
+    }
+    if (k_cache == v_cache || k_scale == v_scale)
+      return fail(QSA_ERR_INVALID_ARG, "K and V need caches and scales of their own");
+  }
+  const int64_t slots = T / block_tokens + 2 * (int64_t)R;
+  if (slots > INT32_MAX) return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != QSA_OK) return st;
+  qsa::kv8::AppendParams p;
+  p.x[0] = static_cast<const uint16_t*>(k);
+  p.x[1] = static_cast<const uint16_t*>(v);
+  p.x_st[0] = k_stride_t;
+  p.x_st[1] = v_stride_t;
+  p.x_sh[0] = k_stride_h;
+  p.x_sh[1] = v_stride_h;
+  p.cache[0] = static_cast<uint8_t*>(k_cache);
+  p.cache[1] = static_cast<uint8_t*>(v_cache);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.block_tokens = block_tokens;
+  p.kv_page_stride = kv_page_stride;
+  p.kv_row_stride = kv_row_stride;
+  p.kv_head_stride = kv_head_stride;
+  p.sc_page_stride = sc_page_stride;
+  p.sc_block_stride = sc_block_stride;
+  p.Hkv = Hkv;
+  p.page_table = page_table;
+  p.pt_stride = pt_stride;
+  p.max_pages = max_pages;
+  p.cu = cu_seqlens_q;
+  p.seq_lens = seq_lens;
+  p.R = R;
+  p.T = T;
+  p.token_weight = token_weight;
+  const dim3 grid((unsigned)slots, (unsigned)Hkv, 2);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (f16) qsa::kv8::append_kernel<true><<<grid, qsa::kv8::APPEND_WARPS * 32, 0, s>>>(p);
+  else qsa::kv8::append_kernel<false><<<grid, qsa::kv8::APPEND_WARPS * 32, 0, s>>>(p);
+  return launch_status("cache append kernel");
+}
+
+#define QSA_APPEND_ARGS                                                                                              \
+  const void *k, int64_t k_stride_t, int64_t k_stride_h, const void *v, int64_t v_stride_t, int64_t v_stride_h,      \
+      void *k_cache, void *v_cache, float *k_scale, float *v_scale, int64_t num_pages, int32_t page_size,            \
+      int32_t block_tokens, int64_t kv_page_stride, int64_t kv_row_stride, int64_t kv_head_stride,                   \
+      int64_t scale_page_stride, int64_t scale_block_stride, int32_t Hkv, const int32_t *page_table,                 \
+      int64_t pt_stride, int32_t max_pages, const int32_t *cu_seqlens_q, const int32_t *seq_lens, int32_t R,         \
+      int64_t T, int64_t *token_weight, void *stream
+#define QSA_APPEND_PASS                                                                                              \
+  k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,    \
+      block_tokens, kv_page_stride, kv_row_stride, kv_head_stride, scale_page_stride, scale_block_stride, Hkv,       \
+      page_table, pt_stride, max_pages, cu_seqlens_q, seq_lens, R, T, token_weight, stream
+
+qsa_status_t qsa_kv_append_fp8(QSA_APPEND_ARGS) { return append_common(QSA_APPEND_PASS, false); }
+qsa_status_t qsa_kv_append_fp8_f16(QSA_APPEND_ARGS) { return append_common(QSA_APPEND_PASS, true); }
+
+size_t qsa_sparse_attention_fp8_workspace_size(int64_t T, int32_t Hq, int32_t Hkv, int32_t width, int32_t weights) {
+  if (T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || width <= 0) return 0;
+  return attn8_layout(T, Hq, Hkv, width, weights != 0).total;
+}
+
+static qsa_status_t attention_fp8_common(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int32_t Hq, const void* k_cache, const void* v_cache,
+    const float* k_scale, const float* v_scale, int64_t num_pages, int32_t page_size, int32_t block_tokens,
+    int64_t kv_page_stride, int64_t kv_row_stride, int64_t kv_head_stride, int64_t sc_page_stride,
+    int64_t sc_block_stride, int32_t Hkv, const int32_t* page_table, int64_t pt_stride, int32_t max_pages,
+    const int32_t* cu_seqlens_q, const int32_t* seq_lens, int32_t R, const int32_t* token_idx, int64_t tok_stride,
+    int32_t width, int64_t T, const float* gate, float scale, void* out, int64_t out_stride_t, float* lse,
+    float* weights, int64_t weights_stride, void* workspace, size_t workspace_bytes, void* stream, bool f16) {
+  using namespace qsa::attn8;
+  qsa_status_t st = check_kv8_sizes(T, R, num_pages, page_size, block_tokens, Hkv, max_pages);
+  if (st != QSA_OK) return st;
+  if (width < 0) return fail(QSA_ERR_INVALID_ARG, "negative width");
+  if (Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > NH)
+    return fail(QSA_ERR_UNSUPPORTED, "Hq = %d, Hkv = %d: Hq must be a multiple of Hkv with at most %d query heads per KV head",
+                Hq, Hkv, NH);
+  if (!std::isfinite(scale)) return fail(QSA_ERR_INVALID_ARG, "scale must be finite");
+  if (T == 0) return ok();
+  if (!q || !cu_seqlens_q || !seq_lens || !out || (width > 0 && !token_idx) || (max_pages > 0 && !page_table))
+    return fail(QSA_ERR_INVALID_ARG, "null pointer argument");
+  st = check_kv8(k_cache, v_cache, k_scale, v_scale, num_pages, page_size, block_tokens, kv_page_stride, kv_row_stride,
+                 kv_head_stride, sc_page_stride, sc_block_stride, Hkv);
+  if (st != QSA_OK) return st;
+  if (!aligned(q, 16) || !aligned(out, 16)) return fail(QSA_ERR_ALIGNMENT, "q and out must be 16-byte aligned");
+  if ((gate && !aligned(gate, 4)) || (lse && !aligned(lse, 4)) || (token_idx && !aligned(token_idx, 4)) ||
+      (page_table && !aligned(page_table, 4)) || (weights && !aligned(weights, 4)) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(seq_lens, 4))
+    return fail(QSA_ERR_ALIGNMENT, "gate, lse, weights and index arrays must be 4-byte aligned");
+  const int64_t strides[3] = {T > 1 ? q_stride_t : 8, Hq > 1 ? q_stride_h : 8, T > 1 ? out_stride_t : 8};
+  for (int64_t s : strides)
+    if (s <= 0 || s % 8 != 0)
+      return fail(QSA_ERR_ALIGNMENT, "strides must be positive multiples of 8 elements (got %lld)", (long long)s);
+  if (Hq > 1 && q_stride_h < D) return fail(QSA_ERR_INVALID_ARG, "q_stride_h below the head dimension 256");
+  if (T > 1 && out_stride_t < (int64_t)Hq * D) return fail(QSA_ERR_INVALID_ARG, "out_stride_t below Hq * 256");
+  if (T > 1 && width > 0 && tok_stride < width) return fail(QSA_ERR_INVALID_ARG, "tok_stride below width");
+  if (T > 1 && weights && weights_stride < width) return fail(QSA_ERR_INVALID_ARG, "weights_stride below width");
+  if (max_pages > 0 && R > 1 && pt_stride < max_pages) return fail(QSA_ERR_INVALID_ARG, "pt_stride below max_pages");
+  {
+    const Range ro = span(out, 2, T, T > 1 ? out_stride_t : 0, Hq, D, 1, 0, D);
+    bool bad = overlaps(ro, span(q, 2, T, T > 1 ? q_stride_t : 0, Hq, Hq > 1 ? q_stride_h : 0, 1, 0, D));
+    for (const void* c : {k_cache, v_cache})
+      bad = bad || overlaps(ro, span(c, 1, num_pages, num_pages > 1 ? kv_page_stride : 0, page_size,
+                                     page_size > 1 ? kv_row_stride : 0, Hkv, Hkv > 1 ? kv_head_stride : 0, D));
+    if (lse) bad = bad || overlaps(span(lse, 4, T, Hq, 1, 0, 1, 0, Hq), ro);
+    if (weights && width > 0) {
+      const Range rw = span(weights, 4, T, T > 1 ? weights_stride : 0, 1, 0, 1, 0, width);
+      bad = bad || overlaps(rw, ro) || overlaps(rw, span(token_idx, 4, T, T > 1 ? tok_stride : 0, 1, 0, 1, 0, width));
+      if (lse) bad = bad || overlaps(rw, span(lse, 4, T, Hq, 1, 0, 1, 0, Hq));
+    }
+    if (bad) return fail(QSA_ERR_INVALID_ARG, "out, lse or weights overlap each other or an input");
+  }
+  const int32_t width1 = width > 0 ? width : 1;
+  const bool want_w = weights != nullptr && width > 0;
+  const Attn8Layout w = attn8_layout(T, Hq, Hkv, width1, weights != nullptr);
+  if (!workspace || workspace_bytes < w.total)
+    return fail(QSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace_bytes, w.total);
+  if (!aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  int32_t splits = 1, tps = 1;
+  attn8_splits(T, Hkv, width1, &splits, &tps);
+  const int64_t ctas = T * Hkv * splits;
+  if (ctas > INT32_MAX || T * Hq > (int64_t)INT32_MAX * 8 || (want_w && T * width > (int64_t)INT32_MAX * 256))
+    return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != QSA_OK) return st;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  Params p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_st = q_stride_t;
+  p.q_sh = q_stride_h;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.k = static_cast<const uint8_t*>(k_cache);
+  p.v = static_cast<const uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.block_tokens = block_tokens;
+  p.kv_page_stride = kv_page_stride;
+  p.kv_row_stride = kv_row_stride;
+  p.kv_head_stride = kv_head_stride;
+  p.sc_page_stride = sc_page_stride;
+  p.sc_block_stride = sc_block_stride;
+  p.page_table = page_table;
+  p.pt_stride = pt_stride;
+  p.max_pages = max_pages;
+  p.cu = cu_seqlens_q;
+  p.seq_lens = seq_lens;
+  p.R = R;
+  p.tok = token_idx;
+  p.tok_stride = T > 1 ? tok_stride : width;
+  p.width = width;
+  p.T = T;
+  p.splits = splits;
+  p.tiles_per_split = tps;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.lse2 = want_w ? reinterpret_cast<float*>(ws + w.lse2) : nullptr;
+  p.part_s = want_w ? reinterpret_cast<float*>(ws + w.s) : nullptr;
+  p.gate = gate;
+  p.out = static_cast<uint16_t*>(out);
+  p.out_st = T > 1 ? out_stride_t : (int64_t)Hq * D;
+  p.lse = lse;
+  p.weights = want_w ? weights : nullptr;
+  p.w_stride = T > 1 ? weights_stride : width;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const unsigned merge = (unsigned)((T * Hq * 32 + 255) / 256);
+  if (f16) {
+    attn_fp8_kernel<true><<<(unsigned)ctas, THREADS, smem_bytes<3>(), s>>>(p);
+    combine_fp8_kernel<true><<<merge, 256, 0, s>>>(p);
+  } else {
+    attn_fp8_kernel<false><<<(unsigned)ctas, THREADS, smem_bytes<2>(), s>>>(p);
+    combine_fp8_kernel<false><<<merge, 256, 0, s>>>(p);
+  }
+  if (want_w) weights_kernel<<<(unsigned)((T * width + 255) / 256), 256, 0, s>>>(p);
+  return launch_status("8-bit cache attention kernels");
+}
+
+#define QSA_ATTN8_ARGS                                                                                               \
+  const void *q, int64_t q_stride_t, int64_t q_stride_h, int32_t Hq, const void *k_cache, const void *v_cache,       \
+      const float *k_scale, const float *v_scale, int64_t num_pages, int32_t page_size, int32_t block_tokens,        \
+      int64_t kv_page_stride, int64_t kv_row_stride, int64_t kv_head_stride, int64_t scale_page_stride,              \
+      int64_t scale_block_stride, int32_t Hkv, const int32_t *page_table, int64_t pt_stride, int32_t max_pages,      \
+      const int32_t *cu_seqlens_q, const int32_t *seq_lens, int32_t R, const int32_t *token_idx, int64_t tok_stride, \
+      int32_t width, int64_t T, const float *gate, float scale, void *out, int64_t out_stride_t, float *lse,         \
+      float *weights, int64_t weights_stride, void *workspace, size_t workspace_bytes, void *stream
+#define QSA_ATTN8_PASS                                                                                               \
+  q, q_stride_t, q_stride_h, Hq, k_cache, v_cache, k_scale, v_scale, num_pages, page_size, block_tokens,             \
+      kv_page_stride, kv_row_stride, kv_head_stride, scale_page_stride, scale_block_stride, Hkv, page_table,         \
+      pt_stride, max_pages, cu_seqlens_q, seq_lens, R, token_idx, tok_stride, width, T, gate, scale, out,            \
+      out_stride_t, lse, weights, weights_stride, workspace, workspace_bytes, stream
+
+qsa_status_t qsa_sparse_attention_fp8(QSA_ATTN8_ARGS) { return attention_fp8_common(QSA_ATTN8_PASS, false); }
+qsa_status_t qsa_sparse_attention_fp8_f16(QSA_ATTN8_ARGS) { return attention_fp8_common(QSA_ATTN8_PASS, true); }
+
+qsa_status_t qsa_accumulate_weights(const float* weights, int64_t weights_stride, const int32_t* token_idx,
+                                    int64_t tok_stride, int32_t width, int64_t T, const int32_t* page_table,
+                                    int64_t pt_stride, int32_t max_pages, const int32_t* cu_seqlens_q,
+                                    const int32_t* seq_lens, int32_t R, int64_t* token_weight, int64_t num_pages,
+                                    int32_t page_size, void* stream) {
+  qsa_status_t st = check_kv8_sizes(T, R, num_pages, page_size, 1, 1, max_pages);
+  if (st != QSA_OK) return st;
+  if (width < 0) return fail(QSA_ERR_INVALID_ARG, "negative width");
+  if (T == 0 || width == 0) return ok();
+  if (!weights || !token_idx || !cu_seqlens_q || !seq_lens || !token_weight || (max_pages > 0 && !page_table))
+    return fail(QSA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(weights, 4) || !aligned(token_idx, 4) || !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) ||
+      (page_table && !aligned(page_table, 4)) || !aligned(token_weight, 8))
+    return fail(QSA_ERR_ALIGNMENT, "weights and index arrays must be 4-byte, token_weight 8-byte aligned");
+  if (T > 1 && (tok_stride < width || weights_stride < width))
+    return fail(QSA_ERR_INVALID_ARG, "tok_stride and weights_stride must be >= width");
+  if (max_pages > 0 && R > 1 && pt_stride < max_pages) return fail(QSA_ERR_INVALID_ARG, "pt_stride below max_pages");
+  {
+    const Range rt = span(token_weight, 8, num_pages, page_size, 1, 0, 1, 0, page_size);
+    if (overlaps(rt, span(weights, 4, T, T > 1 ? weights_stride : 0, 1, 0, 1, 0, width)) ||
+        overlaps(rt, span(token_idx, 4, T, T > 1 ? tok_stride : 0, 1, 0, 1, 0, width)))
+      return fail(QSA_ERR_INVALID_ARG, "token_weight overlaps an input");
+  }
+  const int32_t chunks = (width - 1) / qsa::kv8::ACC_PER_WARP + 1;
+  const int64_t blocks = (T * chunks * 32 + 255) / 256;
+  if (blocks > INT32_MAX) return fail(QSA_ERR_UNSUPPORTED, "too many entries for one launch");
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != QSA_OK) return st;
+  qsa::kv8::AccumulateParams p;
+  p.weights = weights;
+  p.w_stride = T > 1 ? weights_stride : width;
+  p.tok = token_idx;
+  p.tok_stride = T > 1 ? tok_stride : width;
+  p.width = width;
+  p.T = T;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.page_table = page_table;
+  p.pt_stride = pt_stride;
+  p.max_pages = max_pages;
+  p.cu = cu_seqlens_q;
+  p.seq_lens = seq_lens;
+  p.R = R;
+  p.token_weight = reinterpret_cast<unsigned long long*>(token_weight);
+  p.chunks = chunks;
+  qsa::kv8::accumulate_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return launch_status("weight accumulation kernel");
+}
+
+size_t qsa_evict_pages_workspace_size(int32_t R, int32_t max_pages) {
+  if (R <= 0 || max_pages <= 0) return 0;
+  return (size_t)R * (size_t)max_pages * sizeof(uint64_t);
+}
+
+qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int32_t page_size,
+                             const int32_t* page_table, int64_t pt_stride, int32_t max_pages, const int32_t* seq_lens,
+                             const int32_t* keep, int32_t R, int32_t keep_first, int32_t keep_last, int32_t* table_out,
+                             int64_t out_stride, int32_t* freed, int64_t freed_stride, int32_t* counts,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  qsa_status_t st = check_kv8_sizes(0, R, num_pages, page_size, 1, 1, max_pages);
+  if (st != QSA_OK) return st;
+  if (keep_first < 0 || keep_last < 0) return fail(QSA_ERR_INVALID_ARG, "keep_first and keep_last must be non-negative");
+  if (R == 0) return ok();
+  if (!token_weight || !seq_lens || !keep || !counts || (max_pages > 0 && (!page_table || !table_out || !freed)))
+    return fail(QSA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(token_weight, 8) || !aligned(seq_lens, 4) || !aligned(keep, 4) || !aligned(counts, 4) ||
+      !aligned(page_table, 4) || !aligned(table_out, 4) || !aligned(freed, 4))
+    return fail(QSA_ERR_ALIGNMENT, "token_weight must be 8-byte, the index arrays 4-byte aligned");
+  if (max_pages > 0 && R > 1 && (pt_stride < max_pages || out_stride < max_pages || freed_stride < max_pages))
+    return fail(QSA_ERR_INVALID_ARG, "pt_stride, out_stride and freed_stride must be >= max_pages");
+  const size_t need = qsa_evict_pages_workspace_size(R, max_pages);
+  if (max_pages > 0) {
+    const Range rin = span(page_table, 4, R, R > 1 ? pt_stride : 0, 1, 0, 1, 0, max_pages);
+    const Range rout = span(table_out, 4, R, R > 1 ? out_stride : 0, 1, 0, 1, 0, max_pages);
+    const Range rf = span(freed, 4, R, R > 1 ? freed_stride : 0, 1, 0, 1, 0, max_pages);
+    const bool in_place = table_out == page_table && (R == 1 || out_stride == pt_stride);
+    if ((!in_place && overlaps(rin, rout)) || overlaps(rf, rin) || overlaps(rf, rout))
+      return fail(QSA_ERR_INVALID_ARG, "table_out must be page_table itself or apart from it, and freed apart from both");
+    if (!workspace || workspace_bytes < need)
+      return fail(QSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace_bytes, need);
+    if (!aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  }
+  const int64_t pages = (int64_t)R * max_pages;
+  if ((pages * 32 + 255) / 256 > INT32_MAX) return fail(QSA_ERR_UNSUPPORTED, "too many pages for one launch");
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != QSA_OK) return st;
+  qsa::kv8::EvictParams p;
+  p.token_weight = token_weight;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.page_table = page_table;
+  p.pt_stride = R > 1 ? pt_stride : max_pages;
+  p.max_pages = max_pages;
+  p.seq_lens = seq_lens;
+  p.keep = keep;
+  p.R = R;
+  p.keep_first = keep_first;
+  p.keep_last = keep_last;
+  p.table_out = table_out;
+  p.out_stride = R > 1 ? out_stride : max_pages;
+  p.freed = freed;
+  p.freed_stride = R > 1 ? freed_stride : max_pages;
+  p.counts = counts;
+  p.key = static_cast<unsigned long long*>(workspace);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pages > 0) qsa::kv8::page_weight_kernel<<<(unsigned)((pages * 32 + 255) / 256), 256, 0, s>>>(p);
+  qsa::kv8::evict_kernel<<<(unsigned)R, qsa::kv8::EVICT_THREADS, 0, s>>>(p);
+  return launch_status("page eviction kernels");
 }
 
 }  // extern "C"
