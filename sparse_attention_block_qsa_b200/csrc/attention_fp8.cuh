@@ -25,9 +25,17 @@
 //  * Running maximum, sum and output are fp32 in registers (thread = feature
 //    for the output); each tile's O^T is read back from TMEM and added.
 //
-// One CTA per (row, KV head, split of the row's list); the rows are gathered
-// with 16-byte cp.async through the page table into three 32 KB buffers that
-// K and V tiles take in turn.
+// Work is the list of (row, KV head, 128-entry tile) triples in order; every CTA
+// takes an equal contiguous run of it (two CTAs per SM), so any batch fills the
+// GPU to one tile.  A run may begin and end inside a row's list: such pieces go
+// to the workspace and combine_fp8_kernel merges them.  Inside a CTA
+//  * warps 4-7 gather K and V rows with 16-byte cp.async through the page table
+//    into three 32 KB buffers (K and V tiles in turn), two tiles ahead of the
+//    look-ups' consumers, and split each new row's queries;
+//  * warp 8 issues the MMAs, whichever product has its operands: S of tile u + 1
+//    usually runs under the softmax of tile u;
+//  * warps 0-3 run the softmax (thread = entry) and add up the output (thread =
+//    feature); the output product of a tile is read one tile later.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,14 +49,45 @@ namespace attn8 {
 
 constexpr int D = 256;
 constexpr int TILE = 128;              // list entries per tile (UMMA M)
-constexpr int THREADS = 128;           // thread = entry (scores), feature (output)
-constexpr int NH = 16;                 // query heads per KV head, padded
+constexpr int SOFT = 128;              // softmax threads: entry (scores), feature (output)
+constexpr int PROD = 128;              // gathering threads
+constexpr int THREADS = SOFT + PROD + 128;   // the last warpgroup: one warp that issues MMAs
+// Registers a thread: 384 threads twice on an SM leave 80 each at launch; the
+// warpgroups then share them out as 136 + 56 + 48 (the same sum of 240).
+constexpr int REGS_LAUNCH = 80, REGS_SOFT = 136, REGS_PROD = 56, REGS_MMA = 48;
+static_assert(REGS_SOFT + REGS_PROD + REGS_MMA <= 3 * REGS_LAUNCH, "setmaxnreg would wait for ever");
+constexpr int MAX_GROUP = 16;          // query heads per KV head
 constexpr int PT = 3;                  // E4M3 terms of a probability
 constexpr int BUFS = 3;
 constexpr int HALF_BYTES = TILE * 128;       // 128 features of every entry
 constexpr int BUF_BYTES = 2 * HALF_BYTES;
-constexpr int P_BYTES = PT * TILE * NH;
-constexpr int RING = 2;                // tiles whose entry offsets are held
+constexpr int QC_SLOTS = 4;            // rows whose head factors are held
+
+// Sizes of one instance: 16-bit type and query heads held per KV head.
+template <bool F16, int HG>
+struct Cfg {
+  static constexpr int QT = F16 ? 3 : 2;                          // E4M3 terms of a query element
+  static constexpr int QCOLS = QT * HG, QN = (QCOLS + 15) / 16 * 16, QROWS = (QCOLS + 7) / 8 * 8;
+  static constexpr int PCOLS = PT * HG, PN = (PCOLS + 15) / 16 * 16;
+  static constexpr uint32_t TMEM = 2 * QN + 2 * PN <= 128 ? 128 : 256;
+  static constexpr int Q_BYTES = QROWS * D;
+  static constexpr int P_BYTES = PN * TILE;
+  static constexpr size_t SMEM =
+      BUFS * BUF_BYTES + Q_BYTES + P_BYTES + 15 * 8 + 2 * 4 * 17 * 4 + QC_SLOTS * MAX_GROUP * 4 + 16;
+  static constexpr int RESIDENT = 2 * (SMEM + 1024) <= 233472 ? 2 : 1;   // CTAs per SM
+};
+
+// n / d for 0 <= n < 2^31 as a product and a shift.
+struct FastDiv {
+  uint32_t mul;
+  int32_t shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  int l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  return FastDiv{(uint32_t)(((uint64_t(1) << (31 + l)) + d - 1) / d), 31 + l};
+}
+__device__ __forceinline__ int divide(int n, FastDiv f) { return (int)(((uint64_t)(uint32_t)n * f.mul) >> f.shift); }
 
 struct Params {
   const uint16_t* q;          // [T, Hq, 256] bf16 or fp16
@@ -59,7 +98,8 @@ struct Params {
   const float* k_scale;       // [pages, page_size / block_tokens, Hkv]
   const float* v_scale;
   int64_t num_pages;
-  int32_t page_size, block_tokens;
+  int32_t page_size;
+  FastDiv by_page, by_block;  // / page_size, / block_tokens
   int64_t kv_page_stride, kv_row_stride, kv_head_stride;  // bytes
   int64_t sc_page_stride, sc_block_stride;                // elements
   const int32_t* page_table;
@@ -72,10 +112,12 @@ struct Params {
   int64_t tok_stride;
   int32_t width;
   int64_t T;
-  int32_t splits, tiles_per_split;
+  int32_t tiles;              // tiles of one (row, KV head) pair
+  int64_t total;              // tiles of all pairs
+  int32_t ctas;               // runs
   float scale_log2;
-  float* part_o;              // [T, Hkv, splits, group, 256] unnormalised
-  float* part_ml;             // [T, Hkv, splits, group, 2] maximum (log2 units), sum
+  float* part_o;              // [2 ctas, group, 256] unnormalised outputs of pairs cut by a run's ends
+  float* part_ml;             // [2 ctas, group, 2] maximum (log2 units), sum
   float* part_s;              // [T, Hkv, width, group] scores (log2 units), or null
   float* lse2;                // [T, Hq] log2 of the sum of 2^s, or null
   const float* gate;
@@ -86,9 +128,15 @@ struct Params {
   int64_t w_stride;
 };
 
-template <int QT>
-constexpr size_t smem_bytes() {
-  return BUFS * BUF_BYTES + QT * NH * D + P_BYTES + RING * TILE * 8 + 4 * (NH + 4) * 4 + NH * 4 + 32;
+// First tile of run i: the runs differ by at most one tile.
+__device__ __forceinline__ int64_t run_begin(const Params& p, int64_t i) {
+  const int64_t per = p.total / p.ctas, more = p.total % p.ctas;
+  return i * per + (i < more ? i : more);
+}
+// The run that holds tile u.
+__device__ __forceinline__ int64_t run_of(const Params& p, int64_t u) {
+  const int64_t per = p.total / p.ctas, more = p.total % p.ctas;
+  return u < more * (per + 1) ? u / (per + 1) : more + (u - more * (per + 1)) / per;
 }
 
 // Shared-memory descriptor of an unswizzled N-major operand: cores of 8 K
@@ -118,16 +166,32 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// 32 lanes x 8 consecutive columns: thread i gets lane (base + i).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+  static_assert(N % 8 == 0, "columns");
+#pragma unroll
+  for (int i = 0; i < N; i += 8) tmem_ld8(taddr + i, v + i);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 2^-inf = 0
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Arrives on bar once this thread's cp.async copies so far have landed; the
+// barrier counts this arrival like any other.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Two fp32 -> two E4M3 codes (nearest even, saturating); the low byte is a.
@@ -156,6 +220,12 @@ __device__ __forceinline__ float2 widen2(uint32_t x) {
   return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
+template <bool F16>
+__device__ __forceinline__ uint16_t narrow(float x) {
+  if (F16) return __half_as_ushort(__float2half_rn(x));
+  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
 // attn::row_request, with position -1 (nothing visible) for the rows behind
 // the last request's: a batch may be padded.
 __device__ __forceinline__ void row_position(const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_lens,
@@ -164,387 +234,559 @@ __device__ __forceinline__ void row_position(const int32_t* __restrict__ cu, con
   if (t >= (int64_t)__ldg(cu + r + 1)) pos = -1;
 }
 
-template <bool F16>
-__global__ void __launch_bounds__(THREADS, 2) attn_fp8_kernel(const Params p) {
-  constexpr int QT = F16 ? 3 : 2;                   // E4M3 terms of a query element
-  constexpr int QN = QT * NH;
-  constexpr uint32_t S_COLS = QN, O_COLS = PT * NH;
-  constexpr uint32_t TMEM_COLS = S_COLS + 2 * O_COLS <= 128 ? 128 : 256;
+// The entries of consecutive tiles, looked up in stages so that no load is
+// waited for: a tile's list entry two tiles and its page one tile before use.
+// Every lane follows entry `lane_entry` of the tile.
+struct Feed {
+  int64_t t;                  // row, KV head and tile of the stage that loads list entries
+  int g, tile;
+  int64_t left;               // tiles of the run it has not loaded yet
+  const int32_t* pt;          // the row's page table; last token it sees
+  int last;
+  int jA, lastA, gA;          // list entry loaded
+  const int32_t* ptA;
+  int jB, pageB, gB;          // page loaded
+
+  __device__ __forceinline__ void row(const Params& p, int lane) {
+    int r, pos, L;
+    row_position(p.cu, p.seq_lens, p.R, t, lane, r, pos, L);
+    pt = p.page_table + (int64_t)r * p.pt_stride;
+    last = min(pos, L - 1);
+  }
+  __device__ __forceinline__ void load_entry(const Params& p, int lane_entry, int lane) {
+    jA = -1;
+    lastA = last;
+    gA = g;
+    ptA = pt;
+    if (left <= 0) return;
+    --left;
+    const int e = tile * TILE + lane_entry;
+    if (e < p.width) jA = __ldg(p.tok + t * p.tok_stride + e);
+    if (++tile == p.tiles) {
+      tile = 0;
+      if (++g == p.Hkv) {
+        g = 0;
+        ++t;
+        if (left > 0) row(p, lane);
+      }
+    }
+  }
+  __device__ __forceinline__ void load_page(const Params& p) {
+    jB = jA >= 0 && jA <= lastA ? jA : -1;
+    gB = gA;
+    pageB = -1;
+    if (jB >= 0) {
+      const int lp = divide(jB, p.by_page);
+      if (lp < p.max_pages) pageB = __ldg(ptA + lp);
+    }
+  }
+  __device__ __forceinline__ void start(const Params& p, int64_t u0, int64_t n, int lane_entry, int lane) {
+    const int64_t pair = u0 / p.tiles;
+    tile = (int)(u0 - pair * p.tiles);
+    t = pair / p.Hkv;
+    g = (int)(pair - t * p.Hkv);
+    left = n;
+    row(p, lane);
+    load_entry(p, lane_entry, lane);
+    load_page(p);
+    load_entry(p, lane_entry, lane);
+  }
+  // the next tile's entry: its page and token (page < 0: not visible)
+  __device__ __forceinline__ void next(const Params& p, int lane_entry, int lane, int& page, int& j, int& kv_head) {
+    j = jB;
+    kv_head = gB;
+    page = jB >= 0 && (int64_t)pageB < p.num_pages ? pageB : -1;
+    load_page(p);
+    load_entry(p, lane_entry, lane);
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void regs_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <bool F16, int HG>
+__global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_kernel(const Params p) {
+  using C = Cfg<F16, HG>;
+  constexpr int QT = C::QT, QN = C::QN, PN = C::PN;
+  constexpr uint32_t Q_HALF = C::QROWS * 128;
   constexpr uint32_t IDESC_S = idesc_e4m3(TILE, QN, false, false);
-  constexpr uint32_t IDESC_O = idesc_e4m3(128, PT * NH, true, true);
+  constexpr uint32_t IDESC_O = idesc_e4m3(128, PN, true, true);
   extern __shared__ __align__(1024) uint8_t smem8[];   // the swizzle repeats every 1024 bytes
   uint8_t* buf_s = smem8;
-  uint8_t* q_s = buf_s + BUFS * BUF_BYTES;          // [half][QN][128 bytes], swizzled
-  uint8_t* p_s = q_s + QN * D;                      // [term][entry][16 heads]
-  int64_t* off_s = reinterpret_cast<int64_t*>(p_s + P_BYTES);          // [RING][TILE]
-  float* red_s = reinterpret_cast<float*>(off_s + RING * TILE);         // [4 warps][NH + 4]
-  float* qc_s = red_s + 4 * (NH + 4);               // per head: its power of two times scale * log2(e)
-  uint64_t* bar = reinterpret_cast<uint64_t*>(qc_s + NH);               // S done, O done
-  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(bar + 2);
+  uint8_t* q_s = buf_s + BUFS * BUF_BYTES;             // [half][QROWS][128 bytes], swizzled; row = term * HG + head
+  uint8_t* p_s = q_s + C::Q_BYTES;                     // [16 columns][entry][16 bytes]; column = term * HG + head
+  uint64_t* bars = reinterpret_cast<uint64_t*>(p_s + C::P_BYTES);
+  uint64_t *kv_full = bars, *kv_empty = bars + 3, *s_full = bars + 6, *s_empty = bars + 8, *p_full = bars + 10,
+           *o_full = bars + 11, *q_full = bars + 12, *q_empty = bars + 13, *drained = bars + 14;
+  float* red_s = reinterpret_cast<float*>(bars + 15);  // [2][4 warps][17]: tile maxima by head, v_scale
+  float* qc_s = red_s + 2 * 4 * 17;                    // [QC_SLOTS][16]: a head's power of two times scale * log2(e)
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(qc_s + QC_SLOTS * MAX_GROUP);
   int* abort_s = reinterpret_cast<int*>(tmem_s + 1);
+  volatile int* abort = abort_s;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = (int)(blockIdx.x % p.splits);
-  const int g = (int)((blockIdx.x / p.splits) % p.Hkv);
-  const int64_t t = blockIdx.x / ((int64_t)p.splits * p.Hkv);
+  const int64_t u0 = run_begin(p, blockIdx.x), n = run_begin(p, (int64_t)blockIdx.x + 1) - u0;
+  const int64_t pair0 = u0 / p.tiles;
+  const int tile0 = (int)(u0 - pair0 * p.tiles);
 
-  if (warp == 0) tmem_alloc(tmem_s, TMEM_COLS);
+  if (warp == 8) tmem_alloc(tmem_s, C::TMEM);
   if (tid == 0) {
-    mbar_init(&bar[0], 1);
-    mbar_init(&bar[1], 1);
+    for (int i = 0; i < BUFS; ++i) {
+      mbar_init(&kv_full[i], PROD);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 2);
+      mbar_init(&s_empty[i], SOFT);
+    }
+    mbar_init(p_full, SOFT);
+    mbar_init(o_full, 1);
+    mbar_init(q_full, PROD);
+    mbar_init(q_empty, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
     *abort_s = 0;
   }
-
-  int r, pos, L;
-  row_position(p.cu, p.seq_lens, p.R, t, lane, r, pos, L);
-
-  const int e_begin = split * p.tiles_per_split * TILE;
-  const int e_end = min(p.width, e_begin + p.tiles_per_split * TILE);
-  const int ntiles = e_end > e_begin ? (e_end - e_begin + TILE - 1) / TILE : 0;
-  const int32_t* tok_row = p.tok + t * p.tok_stride;
-  const int32_t* pt_row = p.page_table + (int64_t)r * p.pt_stride;
-
-  // Entry tid of tile c: list entry, then page, then pool offset.  The two
-  // dependent loads run one and two tiles ahead of the offset.
-  auto tok_of = [&](int c) -> int {
-    const int e = e_begin + c * TILE + tid;
-    int j = c < ntiles && e < e_end ? __ldg(tok_row + e) : -1;
-    return j > pos || j >= L ? -1 : j;
-  };
-  auto page_of = [&](int j) -> int {
-    if (j < 0) return -1;
-    const int lp = j / p.page_size;
-    const int page = lp < p.max_pages ? __ldg(pt_row + lp) : -1;
-    return (int64_t)page < p.num_pages ? page : -1;
-  };
-  auto off_of = [&](int j, int page) -> int64_t {
-    return page < 0 ? -1 : (int64_t)page * p.kv_page_stride + (int64_t)(j % p.page_size) * p.kv_row_stride +
-                               (int64_t)g * p.kv_head_stride;
-  };
-  auto scale_at = [&](int j, int page) -> int64_t {
-    return page < 0 ? -1 : (int64_t)page * p.sc_page_stride +
-                               (int64_t)((j % p.page_size) / p.block_tokens) * p.sc_block_stride + g;
-  };
-  // gather the K or V rows of tile c into buffer b: 16 threads a row
-  auto load_tile = [&](const uint8_t* base, int c, int b) {
-    if (c < ntiles) {
-      const uint32_t dst = smem_addr(buf_s + b * BUF_BYTES);
-      const int u = tid & 15, n8 = tid >> 4;
-      const uint32_t in_row = (uint32_t)((u >> 3) * HALF_BYTES + (((u & 7) ^ n8) << 4));
-      const int64_t* off = off_s + (c % RING) * TILE;
-#pragma unroll
-      for (int i = 0; i < TILE / 8; ++i) {
-        const int n = i * 8 + n8;
-        const int64_t o = off[n];
-        attn::cp_async16(dst + in_row + n * 128, o >= 0 ? base + o + u * 16 : base, o >= 0);
-      }
-    }
-    attn::cp_async_commit();
-  };
-
-  // offsets of the first two tiles; state of the look-ups that run ahead
-  int j_nx = tok_of(0), page_nx = page_of(j_nx);
-  off_s[tid] = off_of(j_nx, page_nx);
-  int64_t sc0 = scale_at(j_nx, page_nx), sc1;       // scale index of tiles c, c + 1
-  j_nx = tok_of(1);
-  page_nx = page_of(j_nx);
-  off_s[TILE + tid] = off_of(j_nx, page_nx);
-  sc1 = scale_at(j_nx, page_nx);
-  j_nx = tok_of(2);
-  page_nx = page_of(j_nx);                          // tile c + 2
-  int j_nx2 = tok_of(3);                            // tile c + 3
-  __syncthreads();
-  load_tile(p.k, 0, 0);
-  load_tile(p.v, 0, 1);
-  load_tile(p.k, 1, 2);
-
-  // ---- queries: E4M3 terms, heads >= group zero.  Warp w takes heads w, w + 4, ...
-#pragma unroll
-  for (int i = 0; i < NH / 4; ++i) {
-    const int h = warp + 4 * i;
-    uint4 raw4 = make_uint4(0, 0, 0, 0);
-    if (h < p.group)
-      raw4 = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_st + ((int64_t)g * p.group + h) * p.q_sh + lane * 8));
-    float x[8];
-    const uint32_t w4[4] = {raw4.x, raw4.y, raw4.z, raw4.w};
-    float top = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = widen2<F16>(w4[k]);
-      x[2 * k] = f.x;
-      x[2 * k + 1] = f.y;
-      top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-      bad = bad || !(fabsf(f.x) <= 3.4e38f) || !(fabsf(f.y) <= 3.4e38f);
-    }
-    top = warp_max(top);
-    bad = __any_sync(0xffffffffu, bad);
-    // the power of two that brings the largest element into [224, 448]: 448 = 1.75 * 2^8
-    const uint32_t tb = __float_as_uint(top);
-    int e = (int)(tb >> 23) - 127 - 8 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = max(e, -126);
-    const float inv1 = __uint_as_float((uint32_t)(127 + (-e) / 2) << 23);       // 2^(-e) in two factors: it can
-    const float inv2 = __uint_as_float((uint32_t)(127 + (-e) - (-e) / 2) << 23);  // exceed the fp32 range
-    uint32_t term[QT][2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float y[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) y[m] = bad ? __uint_as_float(0x7fc00000u) : x[4 * k + m] * inv1 * inv2;
-#pragma unroll
-      for (int q = 0; q < QT; ++q) {
-        const uint32_t c0 = e4m3x2(y[0], y[1]), c1 = e4m3x2(y[2], y[3]);
-        term[q][k] = c0 | (c1 << 16);
-        const float2 f0 = e4m3x2_value(c0), f1 = e4m3x2_value(c1);
-        y[0] = (y[0] - f0.x) * 16.f;
-        y[1] = (y[1] - f0.y) * 16.f;
-        y[2] = (y[2] - f1.x) * 16.f;
-        y[3] = (y[3] - f1.y) * 16.f;
-      }
-    }
-    const int u = lane >> 1;                        // 16-byte unit of the row
-#pragma unroll
-    for (int q = 0; q < QT; ++q) {
-      const int n = q * NH + h;
-      uint8_t* dst = q_s + (u >> 3) * (QN * 128) + n * 128 + (((u & 7) ^ (n & 7)) << 4) + (lane & 1) * 8;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(term[q][0], term[q][1]);
-    }
-    if (lane == 0) qc_s[h] = h < p.group ? ldexpf(p.scale_log2, e) : 0.f;
-  }
-
-  float m_run[NH], l_run[NH], o0[NH], o1[NH];       // l_run: this thread's entries; o: features tid, 128 + tid
-#pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    m_run[h] = -INFINITY;
-    l_run[h] = o0[h] = o1[h] = 0.f;
-  }
-  float ks = sc0 >= 0 ? __ldg(p.k_scale + sc0) : 0.f, vs = sc0 >= 0 ? __ldg(p.v_scale + sc0) : 0.f;
-  bool seen = sc0 >= 0;
-
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_s;
-  const uint32_t tm_lane = tmem + ((uint32_t)(warp * 32) << 16);
-  const uint64_t q_desc = umma_desc_sw128(smem_addr(q_s));
-  const uint64_t p_desc = desc_plain_mn(smem_addr(p_s), 128, TILE * NH);
-  volatile int* abort = abort_s;
+  const uint32_t tm_o = tmem + 2 * QN;                 // two halves of PN columns
+  // A wait that runs out sets *abort.  Gathering and issuing warps then leave; the softmax warps go on through
+  // their tiles without waiting, so that their barrier is always met.
+  auto gone = [&]() {
+    record_device_error(QSA_DEVERR_WAIT_TIMEOUT);
+    *abort = 1;
+  };
 
-  for (int c = 0; c < ntiles; ++c) {
-    const uint32_t par = c & 1;
-    // ---- S^T = K q^T
-    attn::cp_async_wait<2>();
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (*abort) break;
-    if (tid == 0) {
-      tc_fence_after();
-      const uint64_t kd = umma_desc_sw128(smem_addr(buf_s + ((2 * c) % BUFS) * BUF_BYTES));
+  if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------------------- gather
+    if constexpr (C::RESIDENT > 1) regs_shrink<REGS_PROD>();
+    const int w = warp - 4, entry = 32 * w + lane;
+    const int u = lane & 15, row2 = lane >> 4;         // 16 lanes a row, two rows per instruction
+    Feed f;
+    f.start(p, u0, n, entry, lane);
+    int64_t pair = pair0;
+    int tile = tile0;
+    bool ok = true;
+    // rows of the warp's 32 entries into buffer item % BUFS
+    auto gather = [&](const uint8_t* base, int64_t off, int64_t item) {
+      const int b = (int)(item % BUFS);
+      ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[b], (uint32_t)((item / BUFS) & 1) ^ 1, abort));
+      if (!ok) return;
+      const uint32_t dst = smem_addr(buf_s + b * BUF_BYTES) + (u >> 3) * HALF_BYTES + 32 * w * 128;
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        mma_e4m3(tmem, kd + (s >> 2) * (HALF_BYTES >> 4) + (s & 3) * 2,
-                 q_desc + (s >> 2) * ((QN * 128) >> 4) + (s & 3) * 2, IDESC_S, s > 0);
-      umma_commit(&bar[0]);
-    }
-    // while it runs: offsets of tile c + 2, and the look-ups behind them
-    off_s[((c + 2) % RING) * TILE + tid] = off_of(j_nx, page_nx);
-    const int64_t sc2 = scale_at(j_nx, page_nx);
-    j_nx = j_nx2;
-    page_nx = page_of(j_nx);
-    j_nx2 = tok_of(c + 4);
-    const float ks_nx = sc1 >= 0 ? __ldg(p.k_scale + sc1) : 0.f;
-    const float vs_nx = sc1 >= 0 ? __ldg(p.v_scale + sc1) : 0.f;
-
-    if (!mbar_wait(&bar[0], par, abort)) {
-      record_device_error(QSA_DEVERR_WAIT_TIMEOUT);
-      *abort_s = 1;
-    }
-    tc_fence_after();
-    load_tile(p.v, c + 1, (2 * c) % BUFS);          // K of this tile is consumed
-
-    float x[NH];
-    {
-      float a[NH], b[NH];
-      tmem_ld16(tm_lane, a);
-      tmem_ld16(tm_lane + NH, b);
-      tmem_wait_ld();
+      for (int i = 0; i < 16; ++i) {
+        const int nrow = 2 * i + row2;
+        const int64_t o = __shfl_sync(0xffffffffu, off, nrow);
+        attn::cp_async16(dst + nrow * 128 + (((u & 7) ^ (nrow & 7)) << 4), o >= 0 ? base + o + u * 16 : base, o >= 0);
+      }
+      cp_async_arrive(&kv_full[b]);
+    };
+    // queries of a pair: E4M3 terms; heads at or above the group are zero
+    auto queries = [&](int64_t pr, int nth) {
+      const int64_t t = pr / p.Hkv;
+      const int g = (int)(pr - t * p.Hkv);
+      uint4 x4[HG / 4];
 #pragma unroll
-      for (int h = 0; h < NH; ++h) x[h] = fmaf(b[h], 1.f / 16.f, a[h]);
-      if (QT > 2) {
-        tmem_ld16(tm_lane + 2 * NH, a);
-        tmem_wait_ld();
+      for (int i = 0; i < HG / 4; ++i) {
+        const int h = w + 4 * i;
+        x4[i] = make_uint4(0, 0, 0, 0);
+        if (h < p.group)
+          x4[i] = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_st + ((int64_t)g * p.group + h) * p.q_sh + lane * 8));
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (uint32_t)(nth & 1) ^ 1, abort));
+      if (!ok) return;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) x[h] = fmaf(a[h], 1.f / 256.f, x[h]);
+      for (int i = 0; i < HG / 4; ++i) {
+        const int h = w + 4 * i;
+        const uint32_t w4[4] = {x4[i].x, x4[i].y, x4[i].z, x4[i].w};
+        float x[8];
+        float top = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = widen2<F16>(w4[k]);
+          x[2 * k] = v.x;
+          x[2 * k + 1] = v.y;
+          top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+          bad = bad || !(fabsf(v.x) <= 3.4e38f) || !(fabsf(v.y) <= 3.4e38f);
+        }
+        top = warp_max(top);
+        bad = __any_sync(0xffffffffu, bad);
+        // the power of two that brings the largest element into [224, 448]: 448 = 1.75 * 2^8
+        const uint32_t tb = __float_as_uint(top);
+        int e = (int)(tb >> 23) - 127 - 8 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = max(e, -126);
+        const float inv1 = __uint_as_float((uint32_t)(127 + (-e) / 2) << 23);       // 2^(-e) in two factors:
+        const float inv2 = __uint_as_float((uint32_t)(127 + (-e) - (-e) / 2) << 23);  // one may leave fp32's range
+        uint32_t term[QT][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float y[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) y[m] = bad ? __uint_as_float(0x7fc00000u) : x[4 * k + m] * inv1 * inv2;
+#pragma unroll
+          for (int q = 0; q < QT; ++q) {
+            const uint32_t c0 = e4m3x2(y[0], y[1]), c1 = e4m3x2(y[2], y[3]);
+            term[q][k] = c0 | (c1 << 16);
+            const float2 f0 = e4m3x2_value(c0), f1 = e4m3x2_value(c1);
+            y[0] = (y[0] - f0.x) * 16.f;
+            y[1] = (y[1] - f0.y) * 16.f;
+            y[2] = (y[2] - f1.x) * 16.f;
+            y[3] = (y[3] - f1.y) * 16.f;
+          }
+        }
+        const int un = lane >> 1;                      // 16-byte unit of the row
+#pragma unroll
+        for (int q = 0; q < QT; ++q) {
+          const int nr = q * HG + h;
+          uint8_t* dst = q_s + (un >> 3) * Q_HALF + nr * 128 + (((un & 7) ^ (nr & 7)) << 4) + (lane & 1) * 8;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(term[q][0], term[q][1]);
+        }
+        if (lane == 0) qc_s[(nth % QC_SLOTS) * MAX_GROUP + h] = h < p.group ? ldexpf(p.scale_log2, e) : 0.f;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+    };
+    int nth = 0;                                       // pairs begun
+    for (int64_t k = 0; k < n && ok; ++k) {
+      int page, j, g;
+      f.next(p, entry, lane, page, j, g);
+      const int64_t off = page < 0 ? -1
+                                   : (int64_t)page * p.kv_page_stride +
+                                         (int64_t)(j - divide(j, p.by_page) * p.page_size) * p.kv_row_stride +
+                                         (int64_t)g * p.kv_head_stride;
+      gather(p.k, off, 2 * k);
+      if (ok && (k == 0 || tile == 0)) queries(pair, nth++);
+      if (ok) gather(p.v, off, 2 * k + 1);
+      if (++tile == p.tiles) {
+        tile = 0;
+        ++pair;
       }
     }
+    if (!ok) gone();
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------- MMA issue
+    if constexpr (C::RESIDENT > 1) regs_shrink<REGS_MMA>();
+    if (warp == 8 && lane == 0) {
+      const uint64_t q_desc = umma_desc_sw128(smem_addr(q_s));
+      const uint64_t p_desc = desc_plain_mn(smem_addr(p_s), 128, TILE * 16);
+      int64_t ks = 0, ko = 0;                          // next tile of either product
+      int tile = tile0, nth = 0;                       // of S: tile in its pair, pairs begun
+      bool fresh = true;
+      uint64_t since = global_timer_ns();
+      uint32_t idle = 0;
+      while (ko < n) {
+        bool did = false;
+        if (ks < n && ks <= ko + 1 && mbar_test(&kv_full[(2 * ks) % BUFS], (uint32_t)((2 * ks) / BUFS) & 1) &&
+            mbar_test(&s_empty[ks & 1], (uint32_t)((ks >> 1) & 1) ^ 1) &&
+            (!fresh || mbar_test(q_full, (uint32_t)nth & 1))) {
+          fence_proxy_async_smem();                    // the cp.async writes, before the tensor core reads them
+          tc_fence_after();
+          const int b = (int)((2 * ks) % BUFS);
+          const uint64_t kd = umma_desc_sw128(smem_addr(buf_s + b * BUF_BYTES));
 #pragma unroll
-    for (int h = 0; h < NH; ++h) x[h] = seen ? x[h] * (qc_s[h] * ks) : -INFINITY;
-    if (p.part_s) {
-      const int e = e_begin + c * TILE + tid;
-      if (e < e_end) {
-        float* dst = p.part_s + ((t * p.Hkv + g) * p.width + e) * p.group;
+          for (int s = 0; s < 8; ++s)
+            mma_e4m3(tmem + (uint32_t)(ks & 1) * QN, kd + (s >> 2) * (HALF_BYTES >> 4) + (s & 3) * 2,
+                     q_desc + (s >> 2) * (Q_HALF >> 4) + (s & 3) * 2, IDESC_S, s > 0);
+          umma_commit(&kv_empty[b]);
+          mbar_arrive(&s_full[ks & 1]);                // hands on what q_full published (the head factors)
+          umma_commit(&s_full[ks & 1]);
+          fresh = ++tile == p.tiles;
+          if (fresh) {
+            umma_commit(q_empty);
+            tile = 0;
+            ++nth;
+          }
+          ++ks;
+          did = true;
+        }
+        if (ko < ks && mbar_test(p_full, (uint32_t)ko & 1) &&
+            mbar_test(&kv_full[(2 * ko + 1) % BUFS], (uint32_t)((2 * ko + 1) / BUFS) & 1)) {
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const int b = (int)((2 * ko + 1) % BUFS);
+          const uint64_t vd = umma_desc_sw128(smem_addr(buf_s + b * BUF_BYTES));
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-          if (h < p.group) dst[h] = x[h];
-      }
-    }
-    // ---- maxima over the tile
-    const float vtop = warp_max(vs);
+          for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      const float w = warp_max(x[h]);
-      if (lane == h) red_s[warp * (NH + 4) + h] = w;
-    }
-    if (lane == NH) red_s[warp * (NH + 4) + NH] = vtop;
-    __syncthreads();
-    float alpha[NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      float m = m_run[h];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) m = fmaxf(m, red_s[w * (NH + 4) + h]);
-      const float mr = m == -INFINITY ? 0.f : m;   // nothing visible yet: every probability is 0
-      alpha[h] = exp2f(m_run[h] - mr);
-      x[h] = exp2f(x[h] - mr);
-      m_run[h] = m;
-      l_run[h] = fmaf(l_run[h], alpha[h], x[h]);
-    }
-    float vref = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) vref = fmaxf(vref, red_s[w * (NH + 4) + NH]);
-    // ---- P times v_scale / vref, at most 256, as three E4M3 terms
-    const float vn = vref > 0.f ? vs / vref * 256.f : 0.f;
-#pragma unroll
-    for (int h = 0; h < NH; ++h) x[h] *= vn;
-#pragma unroll
-    for (int q = 0; q < PT; ++q) {
-      uint32_t w4[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t c0 = e4m3x2(x[4 * k], x[4 * k + 1]), c1 = e4m3x2(x[4 * k + 2], x[4 * k + 3]);
-        w4[k] = c0 | (c1 << 16);
-        if (q + 1 < PT) {
-          const float2 f0 = e4m3x2_value(c0), f1 = e4m3x2_value(c1);
-          x[4 * k] = (x[4 * k] - f0.x) * 16.f;
-          x[4 * k + 1] = (x[4 * k + 1] - f0.y) * 16.f;
-          x[4 * k + 2] = (x[4 * k + 2] - f1.x) * 16.f;
-          x[4 * k + 3] = (x[4 * k + 3] - f1.y) * 16.f;
+            for (int s = 0; s < 4; ++s)
+              mma_e4m3(tm_o + hf * PN, vd + hf * (HALF_BYTES >> 4) + s * (32 * 128 >> 4), p_desc + s * (32 * 16 >> 4),
+                       IDESC_O, s > 0);
+          umma_commit(&kv_empty[b]);
+          umma_commit(o_full);
+          ++ko;
+          did = true;
+        }
+        if (did) {
+          idle = 0;
+        } else if ((++idle & 63u) == 0) {
+          if (idle == 64) since = global_timer_ns();
+          if (*abort || global_timer_ns() - since > QSA_WAIT_TIMEOUT_NS) {
+            gone();
+            umma_commit(drained);                      // what it issued still ends before TMEM is freed
+            mbar_wait(drained, 0, nullptr);
+            break;
+          }
         }
       }
-      *reinterpret_cast<uint4*>(p_s + (q * TILE + tid) * NH) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
     }
-    // ---- O^T = V^T P
-    attn::cp_async_wait<2>();
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (*abort) break;
-    if (tid == 0) {
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax
+    if constexpr (C::RESIDENT > 1) regs_grow<REGS_SOFT>();
+    const uint32_t tm_lane = (uint32_t)(warp * 32) << 16;
+    Feed f;
+    f.start(p, u0, n, tid, lane);
+    float l_run[HG], o0[HG], o1[HG];                   // l_run: this thread's entries; o: features tid, 128 + tid
+    float m_lane = -INFINITY, a_prev = 0.f, ov_prev = 0.f, qc = 0.f;   // lane h: head h's maximum, last factor
+    int64_t pair = pair0;
+    int tile = tile0, nth = 0;
+    bool fresh = true;
+    // scales of the next tile's entry: loaded one tile ahead
+    float ks_nx = 0.f, vs_nx = 0.f;
+    bool seen_nx = false;
+    auto scales = [&]() {
+      int page, j, g;
+      f.next(p, tid, lane, page, j, g);
+      seen_nx = page >= 0;
+      ks_nx = vs_nx = 0.f;
+      if (seen_nx) {
+        const int in_page = j - divide(j, p.by_page) * p.page_size;
+        const int64_t at = (int64_t)page * p.sc_page_stride + (int64_t)divide(in_page, p.by_block) * p.sc_block_stride + g;
+        ks_nx = __ldg(p.k_scale + at);
+        vs_nx = __ldg(p.v_scale + at);
+      }
+    };
+    scales();
+    // o = o * a_prev + O^T of tile k
+    auto add_output = [&](int64_t k) {
+      if (!mbar_wait(o_full, (uint32_t)k & 1, abort)) gone();
       tc_fence_after();
-      const uint64_t vd = umma_desc_sw128(smem_addr(buf_s + ((2 * c + 1) % BUFS) * BUF_BYTES));
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+      for (int hf = 0; hf < 2; ++hf) {
+        float d[(C::PCOLS + 7) / 8 * 8];
+        tmem_ld(tm_o + tm_lane + hf * PN, d);
+        tmem_wait_ld();
+        float* o = hf == 0 ? o0 : o1;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          mma_e4m3(tmem + S_COLS + hf * O_COLS, vd + hf * (HALF_BYTES >> 4) + s * (32 * 128 >> 4),
-                   p_desc + s * (32 * NH >> 4), IDESC_O, s > 0);
-      umma_commit(&bar[1]);
-    }
-    if (!mbar_wait(&bar[1], par, abort)) {
-      record_device_error(QSA_DEVERR_WAIT_TIMEOUT);
-      *abort_s = 1;
-    }
-    tc_fence_after();
-    load_tile(p.k, c + 2, (2 * c + 1) % BUFS);      // V of this tile is consumed
-    const float ov = vref * (1.f / 256.f);
+        for (int h = 0; h < HG; ++h) {
+          const float x = fmaf(d[2 * HG + h], 1.f / 256.f, fmaf(d[HG + h], 1.f / 16.f, d[h]));
+          o[h] = fmaf(o[h], __shfl_sync(0xffffffffu, a_prev, h), ov_prev * x);
+        }
+      }
+    };
+    for (int64_t k = 0; k < n; ++k) {
+      const float ks = ks_nx, vs = vs_nx;
+      const bool seen = seen_nx;
+      if (fresh) {
+        m_lane = -INFINITY;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float a[NH], b[NH], d[NH];
-      const uint32_t at = tm_lane + S_COLS + hf * O_COLS;
-      tmem_ld16(at, a);
-      tmem_ld16(at + NH, b);
-      tmem_ld16(at + 2 * NH, d);
-      tmem_wait_ld();
-      float* o = hf == 0 ? o0 : o1;
+        for (int h = 0; h < HG; ++h) l_run[h] = o0[h] = o1[h] = 0.f;
+      }
+      float x[HG];
+      {
+        if (!mbar_wait(&s_full[k & 1], (uint32_t)(k >> 1) & 1, abort)) gone();
+        tc_fence_after();
+        if (fresh) qc = (lane & 15) < HG ? qc_s[(nth % QC_SLOTS) * MAX_GROUP + (lane & 15)] : 0.f;
+        float d[(C::QCOLS + 7) / 8 * 8];
+        tmem_ld(tmem + tm_lane + (uint32_t)(k & 1) * QN, d);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(&s_empty[k & 1]);
 #pragma unroll
-      for (int h = 0; h < NH; ++h)
-        o[h] = fmaf(o[h], alpha[h], ov * fmaf(d[h], 1.f / 256.f, fmaf(b[h], 1.f / 16.f, a[h])));
-    }
-    seen = sc1 >= 0;
-    ks = ks_nx;
-    vs = vs_nx;
-    sc1 = sc2;
-  }
-  attn::cp_async_wait<0>();
+        for (int h = 0; h < HG; ++h) {
+          x[h] = fmaf(d[HG + h], 1.f / 16.f, d[h]);
+          if (QT > 2) x[h] = fmaf(d[(QT - 1) * HG + h], 1.f / 256.f, x[h]);
+          const float c = __shfl_sync(0xffffffffu, qc, h) * ks;
+          x[h] = seen ? x[h] * c : -INFINITY;
+        }
+      }
+      if (p.part_s) {
+        const int e = tile * TILE + tid;
+        if (e < p.width) {
+          float* dst = p.part_s + (pair * p.width + e) * p.group;
+#pragma unroll
+          for (int h = 0; h < HG; ++h)
+            if (h < p.group) dst[h] = x[h];
+        }
+      }
+      scales();                                        // of tile k + 1
+      // ---- maxima over the tile
+      float* red = red_s + (k & 1) * 4 * 17;
+      {
+        float mine = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < HG; ++h) {
+          const float wm = warp_max(x[h]);
+          if (lane == h) mine = wm;
+        }
+        const float vm = warp_max(vs);
+        if (lane == 16) mine = vm;
+        if (lane <= 16) red[warp * 17 + lane] = mine;
+      }
+      named_barrier_sync(1, SOFT);
+      float a_lane, vref;
+      {
+        const int at = lane & 15;
+        const float m = fmaxf(fmaxf(fmaxf(red[at], red[17 + at]), fmaxf(red[34 + at], red[51 + at])), m_lane);
+        vref = fmaxf(fmaxf(red[16], red[33]), fmaxf(red[50], red[67]));
+        a_lane = m == -INFINITY ? 0.f : exp2_fast(m_lane - m);
+        m_lane = m;
+      }
+      const float mr = m_lane == -INFINITY ? 0.f : m_lane;   // nothing visible yet: every probability is 0
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        x[h] = exp2_fast(x[h] - __shfl_sync(0xffffffffu, mr, h));
+        l_run[h] = fmaf(l_run[h], __shfl_sync(0xffffffffu, a_lane, h), x[h]);
+      }
+      // ---- the last tile's output, whose product also frees P
+      if (!fresh) add_output(k - 1);
+      a_prev = a_lane;
+      ov_prev = vref * (1.f / 256.f);
+      // ---- P times v_scale / vref, at most 256, as three E4M3 terms
+      const float vn = vref > 0.f ? __fdividef(vs, vref) * 256.f : 0.f;
+      uint32_t w4[PN / 4];
+#pragma unroll
+      for (int i = 0; i < PN / 4; ++i) w4[i] = 0;
+#pragma unroll
+      for (int c = 0; c < HG / 4; ++c) {
+        float y[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) y[m] = x[4 * c + m] * vn;
+#pragma unroll
+        for (int q = 0; q < PT; ++q) {
+          const uint32_t c0 = e4m3x2(y[0], y[1]), c1 = e4m3x2(y[2], y[3]);
+          w4[q * (HG / 4) + c] = c0 | (c1 << 16);
+          if (q + 1 < PT) {
+            const float2 f0 = e4m3x2_value(c0), f1 = e4m3x2_value(c1);
+            y[0] = (y[0] - f0.x) * 16.f;
+            y[1] = (y[1] - f0.y) * 16.f;
+            y[2] = (y[2] - f1.x) * 16.f;
+            y[3] = (y[3] - f1.y) * 16.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PN / 16; ++i)
+        *reinterpret_cast<uint4*>(p_s + (i * TILE + tid) * 16) =
+            make_uint4(w4[4 * i], w4[4 * i + 1], w4[4 * i + 2], w4[4 * i + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(p_full);
 
-  // ---- the split's maximum, sum and unnormalised output
-  __syncthreads();
+      fresh = ++tile == p.tiles;
+      if (fresh || k + 1 == n) {
+        // ---- end of the pair or of the run: output, or the piece for the merge
+        add_output(k);
+        const bool whole = fresh && (k + 1 >= p.tiles);
+        float* lsum = red_s + (k & 1) * 4 * 17;
+        named_barrier_sync(1, SOFT);                   // every warp has read its maxima
+        float mine = 0.f;
 #pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    float l = l_run[h];
+        for (int h = 0; h < HG; ++h) {
+          float l = l_run[h];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == h) red_s[warp * (NH + 4) + h] = l;
+          for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          if (lane == h) mine = l;
+        }
+        if (lane < 16) lsum[warp * 17 + lane] = mine;
+        named_barrier_sync(1, SOFT);
+        const int at = lane & 15;
+        const float l = lsum[at] + lsum[17 + at] + lsum[34 + at] + lsum[51 + at];
+        const int64_t t = pair / p.Hkv;
+        const int g = (int)(pair - t * p.Hkv);
+        if (whole) {
+          float mul = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
+          const int64_t hq = t * p.Hq + (int64_t)g * p.group;
+          if (p.gate && at < p.group) mul *= 1.f / (1.f + expf(-p.gate[hq + at]));
+          uint16_t* out = p.out + t * p.out_st + (int64_t)g * p.group * D + tid;
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            const float m = __shfl_sync(0xffffffffu, mul, h);
+            if (h < p.group) {
+              out[h * D] = narrow<F16>(o0[h] * m);
+              out[h * D + 128] = narrow<F16>(o1[h] * m);
+            }
+          }
+          if (warp == 0 && lane < p.group) {
+            const float l2 = l == 0.f ? -INFINITY : m_lane + log2f(l);
+            if (p.lse) p.lse[hq + lane] = l2 * 0.69314718055994531f;
+            if (p.lse2) p.lse2[hq + lane] = l2;
+          }
+        } else {
+          // slot 2 i: the pair that run i begins with; 2 i + 1: the one it ends with
+          const int64_t slot = 2 * (int64_t)blockIdx.x + (pair == pair0 ? 0 : 1);
+          float* po = p.part_o + slot * p.group * D + tid;
+#pragma unroll
+          for (int h = 0; h < HG; ++h)
+            if (h < p.group) {
+              po[h * D] = o0[h];
+              po[h * D + 128] = o1[h];
+            }
+          if (warp == 0 && lane < p.group) {
+            p.part_ml[(slot * p.group + lane) * 2] = m_lane;
+            p.part_ml[(slot * p.group + lane) * 2 + 1] = l;
+          }
+        }
+      }
+      if (fresh) {
+        tile = 0;
+        ++pair;
+        ++nth;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
-  const int64_t base = (t * p.Hkv + g) * p.splits + split;
-  float* po = p.part_o + base * p.group * D;
-#pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    if (h < p.group) {
-      po[h * D + tid] = o0[h];
-      po[h * D + 128 + tid] = o1[h];
-      if (tid == h) {
-        float l = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) l += red_s[w * (NH + 4) + h];
-        p.part_ml[(base * p.group + h) * 2] = m_run[h];
-        p.part_ml[(base * p.group + h) * 2 + 1] = l;
-      }
-    }
-  }
-  if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+  if (warp == 8) tmem_dealloc(tmem, C::TMEM);
 }
 
-// One warp per (row, query head): merge the splits, gate, 16-bit output, LSE.
+// Merges the pieces of pairs cut by the end of a run: one warp per (cut, head).
+// The warps of a pair's first cut merge all of its pieces.
 template <bool F16>
 __global__ void __launch_bounds__(256) combine_fp8_kernel(const Params p) {
   const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  if (wid >= p.T * p.Hq) return;
-  const int64_t t = wid / p.Hq;
-  const int h = (int)(wid % p.Hq);
-  const int g = h / p.group, hh = h % p.group;
-  const int64_t base = (t * p.Hkv + g) * p.splits;
+  const int64_t cut = wid / p.group + 1;               // between runs cut - 1 and cut
+  const int hh = (int)(wid % p.group);
+  if (cut >= p.ctas) return;
+  const int64_t at = run_begin(p, cut), pair = at / p.tiles, begin = pair * p.tiles;
+  if (at == begin) return;                             // the runs part between two pairs
+  const int64_t first = run_of(p, begin), last = run_of(p, begin + p.tiles - 1);
+  if (cut != first + 1) return;
   float M = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.part_ml[((base + s) * p.group + hh) * 2]);
+  for (int64_t i = first; i <= last; ++i) {
+    const int64_t slot = 2 * i + (run_begin(p, i) >= begin || i > first ? 0 : 1);
+    M = fmaxf(M, p.part_ml[(slot * p.group + hh) * 2]);
+  }
+  const float Mr = M == -INFINITY ? 0.f : M;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
-  const float Mr = M == -INFINITY ? 0.f : M;
-  for (int s = 0; s < p.splits; ++s) {
-    const float w = exp2f(p.part_ml[((base + s) * p.group + hh) * 2] - Mr);
-    sum = fmaf(w, p.part_ml[((base + s) * p.group + hh) * 2 + 1], sum);
-    const float* po = p.part_o + ((base + s) * p.group + hh) * D + lane * 8;
+  for (int64_t i = first; i <= last; ++i) {
+    const int64_t slot = 2 * i + (run_begin(p, i) >= begin || i > first ? 0 : 1);
+    const float w = exp2f(p.part_ml[(slot * p.group + hh) * 2] - Mr);
+    sum = fmaf(w, p.part_ml[(slot * p.group + hh) * 2 + 1], sum);
+    const float* po = p.part_o + (slot * p.group + hh) * D + lane * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, po[i], acc[i]);
+    for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, po[e], acc[e]);
   }
+  const int64_t t = pair / p.Hkv;
+  const int h = (int)(pair - t * p.Hkv) * p.group + hh;
   float mul = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // a NaN sum stays NaN
   if (p.gate) mul *= 1.f / (1.f + expf(-p.gate[t * p.Hq + h]));
   uint32_t w4[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = acc[2 * i] * mul, b = acc[2 * i + 1] * mul;
-    if (F16) {
-      const __half2 v = __floats2half2_rn(a, b);
-      w4[i] = *reinterpret_cast<const uint32_t*>(&v);
-    } else {
-      w4[i] = attn::pack_bf16(a, b);
-    }
-  }
+  for (int e = 0; e < 4; ++e)
+    w4[e] = (uint32_t)narrow<F16>(acc[2 * e] * mul) | ((uint32_t)narrow<F16>(acc[2 * e + 1] * mul) << 16);
   *reinterpret_cast<uint4*>(p.out + t * p.out_st + (int64_t)h * D + lane * 8) =
       make_uint4(w4[0], w4[1], w4[2], w4[3]);
   if (lane == 0) {

@@ -145,14 +145,31 @@ qsa_status_t device_info(int* sms) {
         {reinterpret_cast<const void*>(qsa::prefill::prefill_kernel<false>), qsa::prefill::SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::prefill::prefill_kernel<true>), qsa::prefill::SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::attn::attn_kernel), qsa::attn::SMEM_BYTES},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false>), qsa::attn8::smem_bytes<2>()},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true>), qsa::attn8::smem_bytes<3>()},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>), qsa::attn8::Cfg<false, 8>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 12>), qsa::attn8::Cfg<false, 12>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 16>), qsa::attn8::Cfg<false, 16>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>), qsa::attn8::Cfg<true, 8>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>), qsa::attn8::Cfg<true, 12>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 16>), qsa::attn8::Cfg<true, 16>::SMEM},
         {reinterpret_cast<const void*>(qsa::topk::topk_rows_kernel), qsa::topk::ROWS_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_pipe_kernel), qsa::topk::PIPE_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_filter_kernel), qsa::topk::TP_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_list_kernel),
          qsa::topk::TP_LIST_WARPS * qsa::topk::tp_list_warp_bytes(qsa::topk::MAX_W)},
     };
+    // These kernels share their launch registers out by setmaxnreg: fewer than they count on would never do.
+    for (const void* fn : {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 12>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 16>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>)}) {
+      cudaFuncAttributes a = {};
+      e = cudaFuncGetAttributes(&a, fn);
+      if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+      if (a.numRegs < qsa::attn8::REGS_LAUNCH)
+        return fail(QSA_ERR_UNSUPPORTED, "attention over the 8-bit cache was built with %d registers a thread; %d needed",
+                    a.numRegs, qsa::attn8::REGS_LAUNCH);
+    }
     for (auto& k : kernels) {
       e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.bytes);
       if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -429,16 +446,11 @@ void attn_splits(int64_t T, int32_t Hkv, int32_t width, int32_t* splits, int32_t
   *cps = (int32_t)per;
 }
 
-// The same for the 8-bit cache's attention: 128-entry tiles, two CTAs per SM.
-void attn8_splits(int64_t T, int32_t Hkv, int32_t width, int32_t* splits, int32_t* tps) {
-  const int64_t tiles = std::max<int64_t>(1, ((int64_t)width + qsa::attn8::TILE - 1) / qsa::attn8::TILE);
-  const int64_t pairs = std::max<int64_t>(1, T * Hkv);
-  int64_t sp = std::min<int64_t>(tiles, std::max<int64_t>(1, 296 / pairs));
-  const int64_t per = (tiles + sp - 1) / sp;
-  sp = (tiles + per - 1) / per;
-  *splits = (int32_t)sp;
-  *tps = (int32_t)per;
-}
+// Runs of the 8-bit cache's attention: two CTAs on each of 148 SMs (a number of
+// its own, so that the workspace depends on the shapes only), no more than tiles.
+constexpr int64_t kAttn8Runs = 296;
+
+int64_t attn8_tiles(int32_t width) { return std::max<int64_t>(1, ((int64_t)width + qsa::attn8::TILE - 1) / qsa::attn8::TILE); }
 
 // Workspace of the 8-bit cache's attention (bytes from its start).
 struct Attn8Layout {
@@ -446,12 +458,11 @@ struct Attn8Layout {
 };
 
 Attn8Layout attn8_layout(int64_t T, int32_t Hq, int32_t Hkv, int32_t width, bool weights) {
-  int32_t splits = 0, tps = 0;
-  attn8_splits(T, Hkv, width, &splits, &tps);
   const size_t heads = (size_t)T * (size_t)Hq;
+  const size_t pieces = 2 * (size_t)std::min(kAttn8Runs, T * Hkv * attn8_tiles(width)) * (size_t)(Hq / Hkv);
   Attn8Layout w;
-  w.ml = heads * splits * qsa::attn8::D * sizeof(float);
-  w.lse2 = w.ml + heads * splits * 2 * sizeof(float);
+  w.ml = pieces * qsa::attn8::D * sizeof(float);
+  w.lse2 = w.ml + pieces * 2 * sizeof(float);
   w.s = w.lse2 + (weights ? heads * sizeof(float) : 0);
   w.total = w.s + (weights ? heads * (size_t)width * sizeof(float) : 0);
   return w;
@@ -1249,6 +1260,17 @@ size_t qsa_sparse_attention_fp8_workspace_size(int64_t T, int32_t Hq, int32_t Hk
   return attn8_layout(T, Hq, Hkv, width, weights != 0).total;
 }
 
+extern "C++" {
+template <bool F16, int HG>
+static void launch_attn8(const qsa::attn8::Params& p, cudaStream_t s) {
+  using C = qsa::attn8::Cfg<F16, HG>;
+  qsa::attn8::attn_fp8_kernel<F16, HG><<<(unsigned)p.ctas, qsa::attn8::THREADS, C::SMEM, s>>>(p);
+  const int64_t warps = (int64_t)(p.ctas - 1) * p.group;   // one per cut between runs and head
+  if (warps > 0 && (p.total % p.ctas != 0 || (p.total / p.ctas) % p.tiles != 0))
+    qsa::attn8::combine_fp8_kernel<F16><<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(p);
+}
+}  // extern "C++"
+
 static qsa_status_t attention_fp8_common(
     const void* q, int64_t q_stride_t, int64_t q_stride_h, int32_t Hq, const void* k_cache, const void* v_cache,
     const float* k_scale, const float* v_scale, int64_t num_pages, int32_t page_size, int32_t block_tokens,
@@ -1261,9 +1283,9 @@ static qsa_status_t attention_fp8_common(
   qsa_status_t st = check_kv8_sizes(T, R, num_pages, page_size, block_tokens, Hkv, max_pages);
   if (st != QSA_OK) return st;
   if (width < 0) return fail(QSA_ERR_INVALID_ARG, "negative width");
-  if (Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > NH)
+  if (Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > MAX_GROUP)
     return fail(QSA_ERR_UNSUPPORTED, "Hq = %d, Hkv = %d: Hq must be a multiple of Hkv with at most %d query heads per KV head",
-                Hq, Hkv, NH);
+                Hq, Hkv, MAX_GROUP);
   if (!std::isfinite(scale)) return fail(QSA_ERR_INVALID_ARG, "scale must be finite");
   if (T == 0) return ok();
   if (!q || !cu_seqlens_q || !seq_lens || !out || (width > 0 && !token_idx) || (max_pages > 0 && !page_table))
@@ -1305,11 +1327,7 @@ static qsa_status_t attention_fp8_common(
   if (!workspace || workspace_bytes < w.total)
     return fail(QSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace_bytes, w.total);
   if (!aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
-  int32_t splits = 1, tps = 1;
-  attn8_splits(T, Hkv, width1, &splits, &tps);
-  const int64_t ctas = T * Hkv * splits;
-  if (ctas > INT32_MAX || T * Hq > (int64_t)INT32_MAX * 8 || (want_w && T * width > (int64_t)INT32_MAX * 256))
-    return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
+  if (want_w && T * width > (int64_t)INT32_MAX * 256) return fail(QSA_ERR_UNSUPPORTED, "too many entries for one launch");
   int sms = 0;
   st = device_info(&sms);
   if (st != QSA_OK) return st;
@@ -1327,7 +1345,8 @@ static qsa_status_t attention_fp8_common(
   p.v_scale = v_scale;
   p.num_pages = num_pages;
   p.page_size = page_size;
-  p.block_tokens = block_tokens;
+  p.by_page = fast_div((uint32_t)page_size);
+  p.by_block = fast_div((uint32_t)block_tokens);
   p.kv_page_stride = kv_page_stride;
   p.kv_row_stride = kv_row_stride;
   p.kv_head_stride = kv_head_stride;
@@ -1343,8 +1362,10 @@ static qsa_status_t attention_fp8_common(
   p.tok_stride = T > 1 ? tok_stride : width;
   p.width = width;
   p.T = T;
-  p.splits = splits;
-  p.tiles_per_split = tps;
+  p.tiles = (int32_t)attn8_tiles(width1);
+  p.total = T * Hkv * p.tiles;
+  const int HG = p.group <= 8 ? 8 : p.group <= 12 ? 12 : 16;
+  p.ctas = (int32_t)std::min<int64_t>(p.total, f16 && HG == 16 ? kAttn8Runs / 2 : kAttn8Runs);
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
@@ -1357,13 +1378,14 @@ static qsa_status_t attention_fp8_common(
   p.weights = want_w ? weights : nullptr;
   p.w_stride = T > 1 ? weights_stride : width;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned merge = (unsigned)((T * Hq * 32 + 255) / 256);
   if (f16) {
-    attn_fp8_kernel<true><<<(unsigned)ctas, THREADS, smem_bytes<3>(), s>>>(p);
-    combine_fp8_kernel<true><<<merge, 256, 0, s>>>(p);
+    if (HG == 8) launch_attn8<true, 8>(p, s);
+    else if (HG == 12) launch_attn8<true, 12>(p, s);
+    else launch_attn8<true, 16>(p, s);
   } else {
-    attn_fp8_kernel<false><<<(unsigned)ctas, THREADS, smem_bytes<2>(), s>>>(p);
-    combine_fp8_kernel<false><<<merge, 256, 0, s>>>(p);
+    if (HG == 8) launch_attn8<false, 8>(p, s);
+    else if (HG == 12) launch_attn8<false, 12>(p, s);
+    else launch_attn8<false, 16>(p, s);
   }
   if (want_w) weights_kernel<<<(unsigned)((T * width + 255) / 256), 256, 0, s>>>(p);
   return launch_status("8-bit cache attention kernels");
