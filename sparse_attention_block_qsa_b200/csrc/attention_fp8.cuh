@@ -26,16 +26,22 @@
 //    for the output); each tile's O^T is read back from TMEM and added.
 //
 // Work is the list of (row, KV head, 128-entry tile) triples in order; every CTA
-// takes an equal contiguous run of it (two CTAs per SM), so any batch fills the
+// takes an equal contiguous run of it (one CTA per SM), so any batch fills the
 // GPU to one tile.  A run may begin and end inside a row's list: such pieces go
 // to the workspace and combine_fp8_kernel merges them.  Inside a CTA
-//  * warps 4-7 gather K and V rows with 16-byte cp.async through the page table
-//    into three 32 KB buffers (K and V tiles in turn), two tiles ahead of the
-//    look-ups' consumers, and split each new row's queries;
-//  * warp 8 issues the MMAs, whichever product has its operands: S of tile u + 1
-//    usually runs under the softmax of tile u;
-//  * warps 0-3 run the softmax (thread = entry) and add up the output (thread =
-//    feature); the output product of a tile is read one tile later.
+//  * warps 8-11 look entries up (list, page table) and gather their K and V rows
+//    with 16-byte cp.async into six 32 KB buffers that K and V tiles take in
+//    turn.  (TMA gathers are no match here: measured 10.7 cycles a 128-byte row
+//    and SM for tile::gather4 and 27 a row for row-wise bulk copies, against 64
+//    bytes a cycle and SM, 19 TB/s out of L2, for cp.async);
+//  * warp 12 issues the MMAs, whichever product has its operands: S runs up to
+//    four tiles ahead of the softmax;
+//  * warps 14 and 15 split each new row's queries;
+//  * warps 0-3 and 4-7 run the softmax, each warpgroup for half of the query
+//    heads (thread = entry, then feature).  Scores are taken relative to a
+//    reference maximum that moves only when a tile exceeds it by 2^4 (or its
+//    v_scale by 1.75): until then a tile needs no reduction, only a vote, and its
+//    output product adds up in TMEM.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -49,33 +55,36 @@ namespace attn8 {
 
 constexpr int D = 256;
 constexpr int TILE = 128;              // list entries per tile (UMMA M)
-constexpr int SOFT = 128;              // softmax threads: entry (scores), feature (output)
+constexpr int TEAM = 128;              // threads of a softmax warpgroup: entry (scores), feature (output)
+constexpr int SOFT = 2 * TEAM;
 constexpr int PROD = 128;              // gathering threads
-constexpr int THREADS = SOFT + PROD + 128;   // the last warpgroup: one warp that issues MMAs
-// Registers a thread: 384 threads twice on an SM leave 80 each at launch; the
-// warpgroups then share them out as 136 + 56 + 48 (the same sum of 240).
-constexpr int REGS_LAUNCH = 80, REGS_SOFT = 136, REGS_PROD = 56, REGS_MMA = 48;
-static_assert(REGS_SOFT + REGS_PROD + REGS_MMA <= 3 * REGS_LAUNCH, "setmaxnreg would wait for ever");
+constexpr int THREADS = SOFT + PROD + 128;   // the last warpgroup: MMA issue, queries
+// A probability is at most 2^REF_SLACK times the reference and v_scale at most
+// V_SLACK times its own; times P_UNIT that is E4M3's largest value.
+constexpr float REF_SLACK = 4.f, V_SLACK = 1.75f, P_UNIT = 16.f;
 constexpr int MAX_GROUP = 16;          // query heads per KV head
 constexpr int PT = 3;                  // E4M3 terms of a probability
-constexpr int BUFS = 3;
+constexpr int BUFS = 6;                // K and V tiles held
+constexpr int S_BUFS = 4;              // score tiles held in TMEM
 constexpr int HALF_BYTES = TILE * 128;       // 128 features of every entry
 constexpr int BUF_BYTES = 2 * HALF_BYTES;
-constexpr int QC_SLOTS = 4;            // rows whose head factors are held
+constexpr int QC_SLOTS = 8;            // rows whose head factors are held: S_BUFS ahead and the current one fit
+constexpr int TH = 8;                  // columns a team has for a term; it fills GH (4, 6 or 8) of them
 
-// Sizes of one instance: 16-bit type and query heads held per KV head.
-template <bool F16, int HG>
+// Sizes of one instance.
+template <bool F16>
 struct Cfg {
-  static constexpr int QT = F16 ? 3 : 2;                          // E4M3 terms of a query element
-  static constexpr int QCOLS = QT * HG, QN = (QCOLS + 15) / 16 * 16, QROWS = (QCOLS + 7) / 8 * 8;
-  static constexpr int PCOLS = PT * HG, PN = (PCOLS + 15) / 16 * 16;
-  static constexpr uint32_t TMEM = 2 * QN + 2 * PN <= 128 ? 128 : 256;
-  static constexpr int Q_BYTES = QROWS * D;
+  static constexpr int QT = F16 ? 3 : 2;          // E4M3 terms of a query element
+  static constexpr int QN = 2 * QT * TH;          // score columns: [team][term][TH heads]
+  static constexpr int PN = 2 * PT * TH;          // output columns, laid out the same way
+  static constexpr uint32_t TMEM = S_BUFS * QN + 2 * PN <= 256 ? 256 : 512;
+  static constexpr int Q_BYTES = QN * D;
   static constexpr int P_BYTES = PN * TILE;
-  static constexpr size_t SMEM =
-      BUFS * BUF_BYTES + Q_BYTES + P_BYTES + 15 * 8 + 2 * 4 * 17 * 4 + QC_SLOTS * MAX_GROUP * 4 + 16;
-  static constexpr int RESIDENT = 2 * (SMEM + 1024) <= 233472 ? 2 : 1;   // CTAs per SM
+  static constexpr int BARS = 2 * BUFS + 2 * S_BUFS + 4 + 3;
+  static constexpr size_t SMEM = BUFS * BUF_BYTES + Q_BYTES + 2 * P_BYTES + BARS * 8 + 8 * (TH + 1) * 4 +
+                                 QC_SLOTS * 2 * TH * 4 + 16;
 };
+static_assert(Cfg<true>::SMEM <= 232448, "shared memory per block");
 
 // n / d for 0 <= n < 2^31 as a product and a shift.
 struct FastDiv {
@@ -100,7 +109,10 @@ struct Params {
   int64_t num_pages;
   int32_t page_size;
   FastDiv by_page, by_block;  // / page_size, / block_tokens
-  int64_t kv_page_stride, kv_row_stride, kv_head_stride;  // bytes
+  // Strides of the cache in rows of `pitch` bytes, the greatest common divisor
+  // of the byte strides: a row's place is a 32-bit number.
+  int64_t pitch;
+  int32_t page_rows, token_rows, head_rows;
   int64_t sc_page_stride, sc_block_stride;                // elements
   const int32_t* page_table;
   int64_t pt_stride;
@@ -157,6 +169,17 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, bool a
   return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -193,6 +216,39 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 2^-inf = 0
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+
+// Whether any of the `threads` threads at barrier `id` says so.
+__device__ __forceinline__ bool barrier_any(uint32_t id, uint32_t threads, bool says) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(says ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t bits2(float2 a) { return *reinterpret_cast<const uint64_t*>(&a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // Two fp32 -> two E4M3 codes (nearest even, saturating); the low byte is a.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
@@ -235,177 +291,281 @@ __device__ __forceinline__ void row_position(const int32_t* __restrict__ cu, con
 }
 
 // The entries of consecutive tiles, looked up in stages so that no load is
-// waited for: a tile's list entry two tiles and its page one tile before use.
-// Every lane follows entry `lane_entry` of the tile.
+// waited for: a tile's list entries two tiles and their pages one tile before
+// use.  Every lane follows the E entries from `entry` of the tile.
+template <int E>
 struct Feed {
-  int64_t t;                  // row, KV head and tile of the stage that loads list entries
-  int g, tile;
-  int64_t left;               // tiles of the run it has not loaded yet
+  int t, g, tile;             // row, KV head and tile of the stage that loads list entries
+  int left;                   // tiles of the run it has not loaded yet
   const int32_t* pt;          // the row's page table; last token it sees
   int last;
-  int jA, lastA, gA;          // list entry loaded
+  int entry, lane;
+  int jA[E], lastA, gA;       // list entries loaded
   const int32_t* ptA;
-  int jB, pageB, gB;          // page loaded
+  int jB[E], pageB[E], gB;    // pages loaded
 
-  __device__ __forceinline__ void row(const Params& p, int lane) {
+  __device__ __forceinline__ void row(const Params& p) {
     int r, pos, L;
     row_position(p.cu, p.seq_lens, p.R, t, lane, r, pos, L);
     pt = p.page_table + (int64_t)r * p.pt_stride;
     last = min(pos, L - 1);
   }
-  __device__ __forceinline__ void load_entry(const Params& p, int lane_entry, int lane) {
-    jA = -1;
+  __device__ __forceinline__ void load_entries(const Params& p) {
     lastA = last;
     gA = g;
     ptA = pt;
+    const int e = tile * TILE + entry;
+    const int32_t* src = p.tok + (int64_t)t * p.tok_stride + e;
+#pragma unroll
+    for (int i = 0; i < E; ++i) jA[i] = left > 0 && e + i < p.width ? __ldg(src + i) : -1;
     if (left <= 0) return;
     --left;
-    const int e = tile * TILE + lane_entry;
-    if (e < p.width) jA = __ldg(p.tok + t * p.tok_stride + e);
     if (++tile == p.tiles) {
       tile = 0;
       if (++g == p.Hkv) {
         g = 0;
         ++t;
-        if (left > 0) row(p, lane);
+        if (left > 0) row(p);
       }
     }
   }
-  __device__ __forceinline__ void load_page(const Params& p) {
-    jB = jA >= 0 && jA <= lastA ? jA : -1;
+  __device__ __forceinline__ void load_pages(const Params& p) {
     gB = gA;
-    pageB = -1;
-    if (jB >= 0) {
-      const int lp = divide(jB, p.by_page);
-      if (lp < p.max_pages) pageB = __ldg(ptA + lp);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      jB[i] = jA[i] <= lastA ? jA[i] : -1;
+      pageB[i] = -1;
+      if (jB[i] >= 0) {
+        const int lp = divide(jB[i], p.by_page);
+        if (lp < p.max_pages) pageB[i] = __ldg(ptA + lp);
+      }
     }
   }
-  __device__ __forceinline__ void start(const Params& p, int64_t u0, int64_t n, int lane_entry, int lane) {
-    const int64_t pair = u0 / p.tiles;
-    tile = (int)(u0 - pair * p.tiles);
+  __device__ __forceinline__ void start(const Params& p, int pair, int tile_, int n, int entry_, int lane_) {
+    entry = entry_;
+    lane = lane_;
+    tile = tile_;
     t = pair / p.Hkv;
-    g = (int)(pair - t * p.Hkv);
+    g = pair - t * p.Hkv;
     left = n;
-    row(p, lane);
-    load_entry(p, lane_entry, lane);
-    load_page(p);
-    load_entry(p, lane_entry, lane);
+    row(p);
+    load_entries(p);
+    load_pages(p);
+    load_entries(p);
   }
-  // the next tile's entry: its page and token (page < 0: not visible)
-  __device__ __forceinline__ void next(const Params& p, int lane_entry, int lane, int& page, int& j, int& kv_head) {
-    j = jB;
+  // the next tile's entries: their pages and tokens (page < 0: not visible)
+  __device__ __forceinline__ void next(const Params& p, int (&page)[E], int (&j)[E], int& kv_head) {
     kv_head = gB;
-    page = jB >= 0 && (int64_t)pageB < p.num_pages ? pageB : -1;
-    load_page(p);
-    load_entry(p, lane_entry, lane);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      j[i] = jB[i];
+      page[i] = (int64_t)pageB[i] < p.num_pages ? pageB[i] : -1;
+    }
+    load_pages(p);
+    load_entries(p);
   }
 };
 
-template <int N>
-__device__ __forceinline__ void regs_grow() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_shrink() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-template <bool F16, int HG>
-__global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_kernel(const Params p) {
-  using C = Cfg<F16, HG>;
+template <bool F16, int GH>
+__global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
+  using C = Cfg<F16>;
   constexpr int QT = C::QT, QN = C::QN, PN = C::PN;
-  constexpr uint32_t Q_HALF = C::QROWS * 128;
+  constexpr uint32_t Q_HALF = QN * 128;
   constexpr uint32_t IDESC_S = idesc_e4m3(TILE, QN, false, false);
   constexpr uint32_t IDESC_O = idesc_e4m3(128, PN, true, true);
   extern __shared__ __align__(1024) uint8_t smem8[];   // the swizzle repeats every 1024 bytes
   uint8_t* buf_s = smem8;
-  uint8_t* q_s = buf_s + BUFS * BUF_BYTES;             // [half][QROWS][128 bytes], swizzled; row = term * HG + head
-  uint8_t* p_s = q_s + C::Q_BYTES;                     // [16 columns][entry][16 bytes]; column = term * HG + head
-  uint64_t* bars = reinterpret_cast<uint64_t*>(p_s + C::P_BYTES);
-  uint64_t *kv_full = bars, *kv_empty = bars + 3, *s_full = bars + 6, *s_empty = bars + 8, *p_full = bars + 10,
-           *o_full = bars + 11, *q_full = bars + 12, *q_empty = bars + 13, *drained = bars + 14;
-  float* red_s = reinterpret_cast<float*>(bars + 15);  // [2][4 warps][17]: tile maxima by head, v_scale
-  float* qc_s = red_s + 2 * 4 * 17;                    // [QC_SLOTS][16]: a head's power of two times scale * log2(e)
-  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(qc_s + QC_SLOTS * MAX_GROUP);
-  int* abort_s = reinterpret_cast<int*>(tmem_s + 1);
-  volatile int* abort = abort_s;
+  uint8_t* q_s = buf_s + BUFS * BUF_BYTES;             // [half][QN][128 bytes], swizzled
+  uint8_t* p_s = q_s + C::Q_BYTES;                     // [2][16 columns][entry][16 bytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(p_s + 2 * C::P_BYTES);
+  uint64_t *kv_full = bars, *kv_empty = kv_full + BUFS, *s_full = kv_empty + BUFS, *s_empty = s_full + S_BUFS,
+           *p_full = s_empty + S_BUFS, *o_full = p_full + 2, *q_full = o_full + 2, *q_empty = q_full + 1,
+           *drained = q_empty + 1;
+  float* red_s = reinterpret_cast<float*>(bars + C::BARS);  // [8 warps][TH + 1]: tile maxima by head, v_scale
+  float* qc_s = red_s + 8 * (TH + 1);                  // [QC_SLOTS][team][TH]: a head's power of two times scale * log2(e)
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(qc_s + QC_SLOTS * 2 * TH);
+  volatile int* abort = reinterpret_cast<int*>(tmem_s + 1);
+  volatile int* add_s = abort + 1;                     // [2] whether an output product adds to what TMEM holds
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t u0 = run_begin(p, blockIdx.x), n = run_begin(p, (int64_t)blockIdx.x + 1) - u0;
-  const int64_t pair0 = u0 / p.tiles;
-  const int tile0 = (int)(u0 - pair0 * p.tiles);
+  const int64_t u0 = run_begin(p, blockIdx.x);
+  const int n = (int)(run_begin(p, (int64_t)blockIdx.x + 1) - u0);
+  const int pair0 = (int)(u0 / p.tiles);
+  const int tile0 = (int)(u0 - (int64_t)pair0 * p.tiles);
 
-  if (warp == 8) tmem_alloc(tmem_s, C::TMEM);
+  if (warp == 12) tmem_alloc(tmem_s, C::TMEM);
   if (tid == 0) {
     for (int i = 0; i < BUFS; ++i) {
       mbar_init(&kv_full[i], PROD);
       mbar_init(&kv_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < S_BUFS; ++i) {
       mbar_init(&s_full[i], 2);
       mbar_init(&s_empty[i], SOFT);
     }
-    mbar_init(p_full, SOFT);
-    mbar_init(o_full, 1);
-    mbar_init(q_full, PROD);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&p_full[i], SOFT);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(q_full, 64);
     mbar_init(q_empty, 1);
     mbar_init(drained, 1);
     fence_mbar_init();
-    *abort_s = 0;
+    *abort = 0;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_s;
-  const uint32_t tm_o = tmem + 2 * QN;                 // two halves of PN columns
+  const uint32_t tm_o = tmem + S_BUFS * QN;            // two halves of PN columns
   // A wait that runs out sets *abort.  Gathering and issuing warps then leave; the softmax warps go on through
-  // their tiles without waiting, so that their barrier is always met.
+  // their tiles without waiting, so that their barriers are always met.
   auto gone = [&]() {
     record_device_error(QSA_DEVERR_WAIT_TIMEOUT);
     *abort = 1;
   };
 
-  if (warp >= 4 && warp < 8) {
+  if (warp >= 8 && warp < 12) {
     // ---------------------------------------------------------------- gather
-    if constexpr (C::RESIDENT > 1) regs_shrink<REGS_PROD>();
-    const int w = warp - 4, entry = 32 * w + lane;
+    const int w = warp - 8;
     const int u = lane & 15, row2 = lane >> 4;         // 16 lanes a row, two rows per instruction
-    Feed f;
-    f.start(p, u0, n, entry, lane);
-    int64_t pair = pair0;
-    int tile = tile0;
-    bool ok = true;
+    Feed<1> f;
+    f.start(p, pair0, tile0, n, 32 * w + lane, lane);
     // rows of the warp's 32 entries into buffer item % BUFS
-    auto gather = [&](const uint8_t* base, int64_t off, int64_t item) {
-      const int b = (int)(item % BUFS);
-      ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[b], (uint32_t)((item / BUFS) & 1) ^ 1, abort));
-      if (!ok) return;
-      const uint32_t dst = smem_addr(buf_s + b * BUF_BYTES) + (u >> 3) * HALF_BYTES + 32 * w * 128;
+    auto gather = [&](const uint8_t* base, int row, int item) -> bool {
+      const int b = item % BUFS;
+      if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[b], (uint32_t)((item / BUFS) & 1) ^ 1, abort))) return false;
+      const uint32_t dst = smem_addr(buf_s + b * BUF_BYTES) + (u >> 3) * HALF_BYTES + (32 * w + row2) * 128;
+      const uint8_t* src = base + u * 16;
+      int rr[16];                                      // all the look-ups before the copies
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int nrow = 2 * i + row2;
-        const int64_t o = __shfl_sync(0xffffffffu, off, nrow);
-        attn::cp_async16(dst + nrow * 128 + (((u & 7) ^ (nrow & 7)) << 4), o >= 0 ? base + o + u * 16 : base, o >= 0);
-      }
+      for (int i = 0; i < 16; ++i) rr[i] = __shfl_sync(0xffffffffu, row, 2 * i + row2);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        attn::cp_async16(dst + i * 256 + (((u & 7) ^ ((2 * i + row2) & 7)) << 4),
+                         src + (int64_t)max(rr[i], 0) * p.pitch, rr[i] >= 0);
       cp_async_arrive(&kv_full[b]);
+      return true;
     };
-    // queries of a pair: E4M3 terms; heads at or above the group are zero
-    auto queries = [&](int64_t pr, int nth) {
-      const int64_t t = pr / p.Hkv;
-      const int g = (int)(pr - t * p.Hkv);
-      uint4 x4[HG / 4];
-#pragma unroll
-      for (int i = 0; i < HG / 4; ++i) {
-        const int h = w + 4 * i;
-        x4[i] = make_uint4(0, 0, 0, 0);
-        if (h < p.group)
-          x4[i] = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_st + ((int64_t)g * p.group + h) * p.q_sh + lane * 8));
+    for (int k = 0; k < n; ++k) {
+      int page[1], j[1], g;
+      f.next(p, page, j, g);
+      const int row = page[0] < 0 ? -1
+                                  : page[0] * p.page_rows +
+                                        (j[0] - divide(j[0], p.by_page) * p.page_size) * p.token_rows + g * p.head_rows;
+      if (!gather(p.k, row, 2 * k) || !gather(p.v, row, 2 * k + 1)) {
+        gone();
+        break;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (uint32_t)(nth & 1) ^ 1, abort));
-      if (!ok) return;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 12) {
+    // ---------------------------------------------------------------- MMA issue
+    // The whole warp goes round, so that descriptors stay in uniform registers; one lane issues.
+    const uint64_t q_desc = umma_desc_sw128(smem_addr(q_s));
+    const uint64_t kv_desc = umma_desc_sw128(smem_addr(buf_s));
+    const uint64_t p_desc = desc_plain_mn(smem_addr(p_s), 128, TILE * 16);
+    int ks = 0, ko = 0;                                // next tile of either product
+    int kb = 0, vb = 1;                                // their buffers
+    uint32_t kp = 0, vp = 0;                           // and those buffers' phases
+    int tile = tile0, nth = 0;                         // of S: tile in its pair, pairs begun
+    bool fresh = true;
+    uint64_t since = global_timer_ns();
+    uint32_t idle = 0;
+    while (ko < n) {
+      bool did = false;
+      if (ko < ks && __all_sync(0xffffffffu, mbar_test(&p_full[ko & 1], (uint32_t)(ko >> 1) & 1) &&
+                                                 mbar_test(&kv_full[vb], vp))) {
+        fence_proxy_async_smem();                      // the cp.async writes, before the tensor core reads them
+        tc_fence_after();
+        const bool add = add_s[ko & 1] != 0;
+        const uint64_t vd = kv_desc + (uint32_t)(vb * (BUF_BYTES >> 4));
+        const uint64_t pd = p_desc + (uint32_t)((ko & 1) * (C::P_BYTES >> 4));
+        if (elect_one()) {
 #pragma unroll
-      for (int i = 0; i < HG / 4; ++i) {
-        const int h = w + 4 * i;
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              mma_e4m3(tm_o + hf * PN, vd + hf * (HALF_BYTES >> 4) + s * (32 * 128 >> 4), pd + s * (32 * 16 >> 4),
+                       IDESC_O, add || s > 0);
+          umma_commit(&kv_empty[vb]);
+          umma_commit(&o_full[ko & 1]);
+        }
+        __syncwarp();
+        ++ko;
+        vb += 2;
+        if (vb >= BUFS) {
+          vb -= BUFS;
+          vp ^= 1;
+        }
+        did = true;
+      }
+      if (ks < n && ks < ko + S_BUFS &&
+          __all_sync(0xffffffffu, mbar_test(&kv_full[kb], kp) &&
+                                      mbar_test(&s_empty[ks % S_BUFS], (uint32_t)((ks / S_BUFS) & 1) ^ 1) &&
+                                      (!fresh || mbar_test(q_full, (uint32_t)nth & 1)))) {
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t kd = kv_desc + (uint32_t)(kb * (BUF_BYTES >> 4));
+        const uint32_t d = tmem + (uint32_t)(ks % S_BUFS) * QN;
+        const bool last = tile + 1 == p.tiles;
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_e4m3(d, kd + (s >> 2) * (HALF_BYTES >> 4) + (s & 3) * 2, q_desc + (s >> 2) * (Q_HALF >> 4) + (s & 3) * 2,
+                     IDESC_S, s > 0);
+          umma_commit(&kv_empty[kb]);
+          mbar_arrive(&s_full[ks % S_BUFS]);           // hands on what q_full published (the head factors)
+          umma_commit(&s_full[ks % S_BUFS]);
+          if (last) umma_commit(q_empty);
+        }
+        __syncwarp();
+        fresh = last;
+        tile = last ? 0 : tile + 1;
+        nth += last ? 1 : 0;
+        ++ks;
+        kb += 2;
+        if (kb >= BUFS) {
+          kb -= BUFS;
+          kp ^= 1;
+        }
+        did = true;
+      }
+      if (did) {
+        idle = 0;
+      } else if ((++idle & 63u) == 0) {
+        if (idle == 64) since = global_timer_ns();
+        if (__any_sync(0xffffffffu, *abort != 0 || global_timer_ns() - since > QSA_WAIT_TIMEOUT_NS)) {
+          gone();
+          if (elect_one()) umma_commit(drained);       // what was issued still ends before TMEM is freed
+          mbar_wait(drained, 0, nullptr);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 14) {
+    // ---------------------------------------------------------------- queries: warp w takes heads w, w + 2, ...
+    const int w = warp - 14;
+    const int pairs = (tile0 + n - 1) / p.tiles + 1;
+    for (int nth = 0; nth < pairs; ++nth) {
+      const int64_t t = (pair0 + nth) / p.Hkv;
+      const int g = pair0 + nth - (int)t * p.Hkv;
+      const uint16_t* q_row = p.q + t * p.q_st + (int64_t)g * p.group * p.q_sh + lane * 8;
+      uint4 x4[TH];                                    // read before the wait; columns past the group are zero
+#pragma unroll
+      for (int i = 0; i < TH; ++i) {
+        const int c = w + 2 * i, hh = c % TH, h = c / TH * GH + hh;
+        x4[i] = make_uint4(0, 0, 0, 0);
+        if (hh < GH && h < p.group) x4[i] = __ldg(reinterpret_cast<const uint4*>(q_row + h * p.q_sh));
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (uint32_t)(nth & 1) ^ 1, abort))) {
+        gone();
+        break;
+      }
+#pragma unroll
+      for (int i = 0; i < TH; ++i) {
+        const int c = w + 2 * i, hh = c % TH, h = c / TH * GH + hh;
         const uint32_t w4[4] = {x4[i].x, x4[i].y, x4[i].z, x4[i].w};
         float x[8];
         float top = 0.f;
@@ -446,295 +606,257 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         const int un = lane >> 1;                      // 16-byte unit of the row
 #pragma unroll
         for (int q = 0; q < QT; ++q) {
-          const int nr = q * HG + h;
+          const int nr = (c / TH) * (QT * TH) + q * TH + hh;
           uint8_t* dst = q_s + (un >> 3) * Q_HALF + nr * 128 + (((un & 7) ^ (nr & 7)) << 4) + (lane & 1) * 8;
           *reinterpret_cast<uint2*>(dst) = make_uint2(term[q][0], term[q][1]);
         }
-        if (lane == 0) qc_s[(nth % QC_SLOTS) * MAX_GROUP + h] = h < p.group ? ldexpf(p.scale_log2, e) : 0.f;
+        if (lane == 0) qc_s[(nth % QC_SLOTS) * 2 * TH + c] = hh < GH && h < p.group ? ldexpf(p.scale_log2, e) : 0.f;
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
-    };
-    int nth = 0;                                       // pairs begun
-    for (int64_t k = 0; k < n && ok; ++k) {
-      int page, j, g;
-      f.next(p, entry, lane, page, j, g);
-      const int64_t off = page < 0 ? -1
-                                   : (int64_t)page * p.kv_page_stride +
-                                         (int64_t)(j - divide(j, p.by_page) * p.page_size) * p.kv_row_stride +
-                                         (int64_t)g * p.kv_head_stride;
-      gather(p.k, off, 2 * k);
-      if (ok && (k == 0 || tile == 0)) queries(pair, nth++);
-      if (ok) gather(p.v, off, 2 * k + 1);
-      if (++tile == p.tiles) {
-        tile = 0;
-        ++pair;
-      }
     }
-    if (!ok) gone();
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp >= 8) {
-    // ---------------------------------------------------------------- MMA issue
-    if constexpr (C::RESIDENT > 1) regs_shrink<REGS_MMA>();
-    if (warp == 8 && lane == 0) {
-      const uint64_t q_desc = umma_desc_sw128(smem_addr(q_s));
-      const uint64_t p_desc = desc_plain_mn(smem_addr(p_s), 128, TILE * 16);
-      int64_t ks = 0, ko = 0;                          // next tile of either product
-      int tile = tile0, nth = 0;                       // of S: tile in its pair, pairs begun
-      bool fresh = true;
-      uint64_t since = global_timer_ns();
-      uint32_t idle = 0;
-      while (ko < n) {
-        bool did = false;
-        if (ks < n && ks <= ko + 1 && mbar_test(&kv_full[(2 * ks) % BUFS], (uint32_t)((2 * ks) / BUFS) & 1) &&
-            mbar_test(&s_empty[ks & 1], (uint32_t)((ks >> 1) & 1) ^ 1) &&
-            (!fresh || mbar_test(q_full, (uint32_t)nth & 1))) {
-          fence_proxy_async_smem();                    // the cp.async writes, before the tensor core reads them
-          tc_fence_after();
-          const int b = (int)((2 * ks) % BUFS);
-          const uint64_t kd = umma_desc_sw128(smem_addr(buf_s + b * BUF_BYTES));
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_e4m3(tmem + (uint32_t)(ks & 1) * QN, kd + (s >> 2) * (HALF_BYTES >> 4) + (s & 3) * 2,
-                     q_desc + (s >> 2) * (Q_HALF >> 4) + (s & 3) * 2, IDESC_S, s > 0);
-          umma_commit(&kv_empty[b]);
-          mbar_arrive(&s_full[ks & 1]);                // hands on what q_full published (the head factors)
-          umma_commit(&s_full[ks & 1]);
-          fresh = ++tile == p.tiles;
-          if (fresh) {
-            umma_commit(q_empty);
-            tile = 0;
-            ++nth;
-          }
-          ++ks;
-          did = true;
-        }
-        if (ko < ks && mbar_test(p_full, (uint32_t)ko & 1) &&
-            mbar_test(&kv_full[(2 * ko + 1) % BUFS], (uint32_t)((2 * ko + 1) / BUFS) & 1)) {
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const int b = (int)((2 * ko + 1) % BUFS);
-          const uint64_t vd = umma_desc_sw128(smem_addr(buf_s + b * BUF_BYTES));
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_e4m3(tm_o + hf * PN, vd + hf * (HALF_BYTES >> 4) + s * (32 * 128 >> 4), p_desc + s * (32 * 16 >> 4),
-                       IDESC_O, s > 0);
-          umma_commit(&kv_empty[b]);
-          umma_commit(o_full);
-          ++ko;
-          did = true;
-        }
-        if (did) {
-          idle = 0;
-        } else if ((++idle & 63u) == 0) {
-          if (idle == 64) since = global_timer_ns();
-          if (*abort || global_timer_ns() - since > QSA_WAIT_TIMEOUT_NS) {
-            gone();
-            umma_commit(drained);                      // what it issued still ends before TMEM is freed
-            mbar_wait(drained, 0, nullptr);
-            break;
-          }
-        }
-      }
-    }
-    __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- softmax
-    if constexpr (C::RESIDENT > 1) regs_grow<REGS_SOFT>();
-    const uint32_t tm_lane = (uint32_t)(warp * 32) << 16;
-    Feed f;
-    f.start(p, u0, n, tid, lane);
-    float l_run[HG], o0[HG], o1[HG];                   // l_run: this thread's entries; o: features tid, 128 + tid
-    float m_lane = -INFINITY, a_prev = 0.f, ov_prev = 0.f, qc = 0.f;   // lane h: head h's maximum, last factor
-    int64_t pair = pair0;
-    int tile = tile0, nth = 0;
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- softmax: a team for each half of the heads
+    const int team = warp >> 2, e_tid = tid & (TEAM - 1);
+    const uint32_t tm_lane = (uint32_t)((warp & 3) * 32) << 16;
+    const int heads = min(GH, p.group - team * GH);    // of this team (may be below 1: nothing to write)
+    Feed<1> f;
+    f.start(p, pair0, tile0, n, e_tid, lane);
+    // heads 2 i, 2 i + 1: sums over this thread's entries; features e_tid and 128 + e_tid
+    float2 l_run[GH / 2], o0[GH / 2], o1[GH / 2];
+    float mref[GH];                                    // same in every thread of the team
+    float vref = 0.f, vinv = 0.f;
+    bool set = false;                                  // mref holds maxima: a tile had a visible entry
+    bool add = false;                                  // TMEM holds output of this pair that o0, o1 lack
+    int pair = pair0, tile = tile0, nth = 0;
     bool fresh = true;
     // scales of the next tile's entry: loaded one tile ahead
     float ks_nx = 0.f, vs_nx = 0.f;
     bool seen_nx = false;
     auto scales = [&]() {
-      int page, j, g;
-      f.next(p, tid, lane, page, j, g);
-      seen_nx = page >= 0;
-      ks_nx = vs_nx = 0.f;
-      if (seen_nx) {
-        const int in_page = j - divide(j, p.by_page) * p.page_size;
-        const int64_t at = (int64_t)page * p.sc_page_stride + (int64_t)divide(in_page, p.by_block) * p.sc_block_stride + g;
-        ks_nx = __ldg(p.k_scale + at);
-        vs_nx = __ldg(p.v_scale + at);
-      }
+      int page[1], j[1], g;
+      f.next(p, page, j, g);
+      seen_nx = page[0] >= 0;
+      const int in_page = j[0] - divide(j[0], p.by_page) * p.page_size;
+      const int64_t at = seen_nx ? (int64_t)page[0] * p.sc_page_stride +
+                                       (int64_t)divide(in_page, p.by_block) * p.sc_block_stride + g
+                                 : 0;
+      ks_nx = __ldg(p.k_scale + at);                   // element 0 always exists; unseen entries do not use it
+      vs_nx = __ldg(p.v_scale + at);
     };
     scales();
-    // o = o * a_prev + O^T of tile k
-    auto add_output = [&](int64_t k) {
-      if (!mbar_wait(o_full, (uint32_t)k & 1, abort)) gone();
+    auto output_done = [&](int k) {                    // tile k's product is in TMEM, its P free
+      if (!mbar_wait(&o_full[k & 1], (uint32_t)(k >> 1) & 1, abort)) gone();
       tc_fence_after();
+    };
+    auto take_output = [&]() {                         // o += what TMEM holds
+      const float2 unit = both(vref * (1.f / P_UNIT));
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float d[(C::PCOLS + 7) / 8 * 8];
-        tmem_ld(tm_o + tm_lane + hf * PN, d);
+        float d[PT * TH];
+        tmem_ld(tm_o + tm_lane + hf * PN + team * PT * TH, d);
         tmem_wait_ld();
-        float* o = hf == 0 ? o0 : o1;
+        float2* o = hf == 0 ? o0 : o1;
 #pragma unroll
-        for (int h = 0; h < HG; ++h) {
-          const float x = fmaf(d[2 * HG + h], 1.f / 256.f, fmaf(d[HG + h], 1.f / 16.f, d[h]));
-          o[h] = fmaf(o[h], __shfl_sync(0xffffffffu, a_prev, h), ov_prev * x);
+        for (int i = 0; i < GH / 2; ++i) {
+          float2 x = make_float2(d[2 * i], d[2 * i + 1]);
+          x = fma2(make_float2(d[TH + 2 * i], d[TH + 2 * i + 1]), both(1.f / 16.f), x);
+          x = fma2(make_float2(d[2 * TH + 2 * i], d[2 * TH + 2 * i + 1]), both(1.f / 256.f), x);
+          o[i] = fma2(x, unit, o[i]);
         }
       }
     };
-    for (int64_t k = 0; k < n; ++k) {
-      const float ks = ks_nx, vs = vs_nx;
+    for (int k = 0; k < n; ++k) {
       const bool seen = seen_nx;
-      if (fresh) {
-        m_lane = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < HG; ++h) l_run[h] = o0[h] = o1[h] = 0.f;
-      }
-      float x[HG];
+      const float ks = ks_nx, vs = seen ? vs_nx : 0.f;
+      float2 x[GH / 2];                                // scores, then relative to mref, then probabilities
       {
-        if (!mbar_wait(&s_full[k & 1], (uint32_t)(k >> 1) & 1, abort)) gone();
+        if (!mbar_wait(&s_full[k % S_BUFS], (uint32_t)(k / S_BUFS) & 1, abort)) gone();
         tc_fence_after();
-        if (fresh) qc = (lane & 15) < HG ? qc_s[(nth % QC_SLOTS) * MAX_GROUP + (lane & 15)] : 0.f;
-        float d[(C::QCOLS + 7) / 8 * 8];
-        tmem_ld(tmem + tm_lane + (uint32_t)(k & 1) * QN, d);
+        if (fresh) {
+#pragma unroll
+          for (int h = 0; h < GH; ++h) mref[h] = 0.f;
+#pragma unroll
+          for (int i = 0; i < GH / 2; ++i) l_run[i] = o0[i] = o1[i] = make_float2(0.f, 0.f);
+          vref = vinv = 0.f;
+          add = set = false;
+        }
+        const float2* qc = reinterpret_cast<const float2*>(qc_s + ((nth % QC_SLOTS) * 2 + team) * TH);
+        float d[QT * TH];
+        tmem_ld(tmem + tm_lane + (uint32_t)(k % S_BUFS) * QN + team * QT * TH, d);
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive(&s_empty[k & 1]);
+        mbar_arrive(&s_empty[k % S_BUFS]);
 #pragma unroll
-        for (int h = 0; h < HG; ++h) {
-          x[h] = fmaf(d[HG + h], 1.f / 16.f, d[h]);
-          if (QT > 2) x[h] = fmaf(d[(QT - 1) * HG + h], 1.f / 256.f, x[h]);
-          const float c = __shfl_sync(0xffffffffu, qc, h) * ks;
-          x[h] = seen ? x[h] * c : -INFINITY;
+        for (int i = 0; i < GH / 2; ++i) {
+          x[i] = fma2(make_float2(d[TH + 2 * i], d[TH + 2 * i + 1]), both(1.f / 16.f), make_float2(d[2 * i], d[2 * i + 1]));
+          if (QT > 2)
+            x[i] = fma2(make_float2(d[(QT - 1) * TH + 2 * i], d[(QT - 1) * TH + 2 * i + 1]), both(1.f / 256.f), x[i]);
+          x[i] = mul2(x[i], mul2(qc[i], both(ks)));
+          if (!seen) x[i] = make_float2(-INFINITY, -INFINITY);
         }
       }
       if (p.part_s) {
-        const int e = tile * TILE + tid;
+        const int e = tile * TILE + e_tid;
         if (e < p.width) {
-          float* dst = p.part_s + (pair * p.width + e) * p.group;
+          float* dst = p.part_s + ((int64_t)pair * p.width + e) * p.group + team * GH;
 #pragma unroll
-          for (int h = 0; h < HG; ++h)
-            if (h < p.group) dst[h] = x[h];
+          for (int h = 0; h < GH; ++h)
+            if (h < heads) dst[h] = h & 1 ? x[h / 2].y : x[h / 2].x;
         }
       }
-      scales();                                        // of tile k + 1
-      // ---- maxima over the tile
-      float* red = red_s + (k & 1) * 4 * 17;
-      {
+      float over = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < GH / 2; ++i) {
+        x[i] = add2(x[i], make_float2(-mref[2 * i], -mref[2 * i + 1]));
+        over = fmaxf(over, fmaxf(x[i].x, x[i].y));
+      }
+      // one vote for both teams: whether an output product adds is common to all columns
+      if (barrier_any(1, SOFT, !set || over > REF_SLACK || vs > V_SLACK * vref)) {
+        // ---- new references: the tile's maxima where they are larger
         float mine = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < HG; ++h) {
-          const float wm = warp_max(x[h]);
+        for (int h = 0; h < GH; ++h) {
+          const float wm = warp_max((h & 1 ? x[h / 2].y : x[h / 2].x) + mref[h]);
           if (lane == h) mine = wm;
         }
         const float vm = warp_max(vs);
-        if (lane == 16) mine = vm;
-        if (lane <= 16) red[warp * 17 + lane] = mine;
-      }
-      named_barrier_sync(1, SOFT);
-      float a_lane, vref;
-      {
-        const int at = lane & 15;
-        const float m = fmaxf(fmaxf(fmaxf(red[at], red[17 + at]), fmaxf(red[34 + at], red[51 + at])), m_lane);
-        vref = fmaxf(fmaxf(red[16], red[33]), fmaxf(red[50], red[67]));
-        a_lane = m == -INFINITY ? 0.f : exp2_fast(m_lane - m);
-        m_lane = m;
-      }
-      const float mr = m_lane == -INFINITY ? 0.f : m_lane;   // nothing visible yet: every probability is 0
+        if (lane == TH) mine = vm;
+        if (lane <= TH) red_s[warp * (TH + 1) + lane] = mine;
+        named_barrier_sync(2 + team, TEAM);
+        const float* red = red_s + team * 4 * (TH + 1);
+        if (add) {
+          output_done(k - 1);
+          take_output();
+          add = false;
+        }
+        auto of_team = [&](int c) {
+          return fmaxf(fmaxf(red[c], red[TH + 1 + c]), fmaxf(red[2 * (TH + 1) + c], red[3 * (TH + 1) + c]));
+        };
+        vref = fmaxf(vref, of_team(TH));
+        vinv = vref > 0.f ? 1.f / vref : 0.f;
+        bool any = false;
 #pragma unroll
-      for (int h = 0; h < HG; ++h) {
-        x[h] = exp2_fast(x[h] - __shfl_sync(0xffffffffu, mr, h));
-        l_run[h] = fmaf(l_run[h], __shfl_sync(0xffffffffu, a_lane, h), x[h]);
-      }
-      // ---- the last tile's output, whose product also frees P
-      if (!fresh) add_output(k - 1);
-      a_prev = a_lane;
-      ov_prev = vref * (1.f / 256.f);
-      // ---- P times v_scale / vref, at most 256, as three E4M3 terms
-      const float vn = vref > 0.f ? __fdividef(vs, vref) * 256.f : 0.f;
-      uint32_t w4[PN / 4];
+        for (int i = 0; i < GH / 2; ++i) {
+          float a[2];
 #pragma unroll
-      for (int i = 0; i < PN / 4; ++i) w4[i] = 0;
-#pragma unroll
-      for (int c = 0; c < HG / 4; ++c) {
-        float y[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) y[m] = x[4 * c + m] * vn;
-#pragma unroll
-        for (int q = 0; q < PT; ++q) {
-          const uint32_t c0 = e4m3x2(y[0], y[1]), c1 = e4m3x2(y[2], y[3]);
-          w4[q * (HG / 4) + c] = c0 | (c1 << 16);
-          if (q + 1 < PT) {
-            const float2 f0 = e4m3x2_value(c0), f1 = e4m3x2_value(c1);
-            y[0] = (y[0] - f0.x) * 16.f;
-            y[1] = (y[1] - f0.y) * 16.f;
-            y[2] = (y[2] - f1.x) * 16.f;
-            y[3] = (y[3] - f1.y) * 16.f;
+          for (int e = 0; e < 2; ++e) {
+            const int h = 2 * i + e;
+            float m = of_team(h);
+            any = any || m > -INFINITY;
+            if (set) m = fmaxf(m, mref[h]);
+            if (!(m > -INFINITY)) m = 0.f;             // nothing visible yet (or only NaN)
+            a[e] = mref[h] - m;
+            mref[h] = m;
           }
+          x[i] = add2(x[i], make_float2(a[0], a[1]));
+          const float2 alpha = set ? make_float2(exp2_fast(a[0]), exp2_fast(a[1])) : both(1.f);
+          l_run[i] = mul2(l_run[i], alpha);
+          o0[i] = mul2(o0[i], alpha);
+          o1[i] = mul2(o1[i], alpha);
+        }
+        set = set || any;
+        named_barrier_sync(2 + team, TEAM);            // red_s may be written again
+      }
+      scales();                                        // of tile k + 1
+      // ---- P times v_scale / vref as three E4M3 terms
+      const float2 vn = both(vs * vinv * P_UNIT);
+      uint32_t w2[PT][2];
+#pragma unroll
+      for (int q = 0; q < PT; ++q) w2[q][1] = 0;
+      float2 y[TH / 2];
+#pragma unroll
+      for (int i = 0; i < TH / 2; ++i) {
+        y[i] = make_float2(0.f, 0.f);
+        if (i < GH / 2) {
+          const float2 pr = make_float2(exp2_fast(x[i].x), exp2_fast(x[i].y));
+          l_run[i] = add2(l_run[i], pr);
+          y[i] = mul2(pr, vn);
         }
       }
 #pragma unroll
-      for (int i = 0; i < PN / 16; ++i)
-        *reinterpret_cast<uint4*>(p_s + (i * TILE + tid) * 16) =
-            make_uint4(w4[4 * i], w4[4 * i + 1], w4[4 * i + 2], w4[4 * i + 3]);
+      for (int q = 0; q < PT; ++q) {
+        uint32_t c[TH / 2];
+#pragma unroll
+        for (int i = 0; i < TH / 2; ++i) {
+          c[i] = 0;
+          if (i < GH / 2) {
+            c[i] = e4m3x2(y[i].x, y[i].y);
+            if (q + 1 < PT) y[i] = fma2(e4m3x2_value(c[i]), both(-16.f), mul2(y[i], both(16.f)));
+          }
+        }
+        w2[q][0] = c[0] | (c[1] << 16);
+        w2[q][1] = c[2] | (c[3] << 16);
+      }
+      if (k > 1) output_done(k - 2);
+      uint8_t* dst = p_s + (k & 1) * C::P_BYTES + e_tid * 16;
+#pragma unroll
+      for (int q = 0; q < PT; ++q) {
+        const int col = (team * PT + q) * TH;          // columns col .. col + 7: half of a 16-byte unit
+        *reinterpret_cast<uint2*>(dst + (col / 16) * (TILE * 16) + (col % 16)) = make_uint2(w2[q][0], w2[q][1]);
+      }
+      if (tid == 0) add_s[k & 1] = add ? 1 : 0;
+      add = true;
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(p_full);
+      mbar_arrive(&p_full[k & 1]);
 
       fresh = ++tile == p.tiles;
       if (fresh || k + 1 == n) {
         // ---- end of the pair or of the run: output, or the piece for the merge
-        add_output(k);
-        const bool whole = fresh && (k + 1 >= p.tiles);
-        float* lsum = red_s + (k & 1) * 4 * 17;
-        named_barrier_sync(1, SOFT);                   // every warp has read its maxima
-        float mine = 0.f;
+        output_done(k);
+        take_output();
+        const bool whole = fresh && k + 1 >= p.tiles;
+        float mine = 0.f, mref_lane = 0.f;             // of head `lane`
 #pragma unroll
-        for (int h = 0; h < HG; ++h) {
-          float l = l_run[h];
+        for (int h = 0; h < GH; ++h) {
+          float l = h & 1 ? l_run[h / 2].y : l_run[h / 2].x;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-          if (lane == h) mine = l;
+          if (lane == h) {
+            mine = l;
+            mref_lane = mref[h];
+          }
         }
-        if (lane < 16) lsum[warp * 17 + lane] = mine;
-        named_barrier_sync(1, SOFT);
-        const int at = lane & 15;
-        const float l = lsum[at] + lsum[17 + at] + lsum[34 + at] + lsum[51 + at];
+        if (lane < TH) red_s[warp * (TH + 1) + lane] = mine;
+        named_barrier_sync(2 + team, TEAM);
+        const int at = lane & (TH - 1);
+        const float* red = red_s + team * 4 * (TH + 1) + at;
+        const float l = red[0] + red[TH + 1] + red[2 * (TH + 1)] + red[3 * (TH + 1)];
+        named_barrier_sync(2 + team, TEAM);
         const int64_t t = pair / p.Hkv;
-        const int g = (int)(pair - t * p.Hkv);
+        const int g = pair - (int)t * p.Hkv;
         if (whole) {
           float mul = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
-          const int64_t hq = t * p.Hq + (int64_t)g * p.group;
-          if (p.gate && at < p.group) mul *= 1.f / (1.f + expf(-p.gate[hq + at]));
-          uint16_t* out = p.out + t * p.out_st + (int64_t)g * p.group * D + tid;
+          const int64_t hq = t * p.Hq + (int64_t)g * p.group + team * GH;
+          if (p.gate && at < heads) mul *= 1.f / (1.f + expf(-p.gate[hq + at]));
+          uint16_t* out = p.out + t * p.out_st + ((int64_t)g * p.group + team * GH) * D + e_tid;
 #pragma unroll
-          for (int h = 0; h < HG; ++h) {
+          for (int h = 0; h < GH; ++h) {
             const float m = __shfl_sync(0xffffffffu, mul, h);
-            if (h < p.group) {
-              out[h * D] = narrow<F16>(o0[h] * m);
-              out[h * D + 128] = narrow<F16>(o1[h] * m);
+            if (h < heads) {
+              out[h * D] = narrow<F16>((h & 1 ? o0[h / 2].y : o0[h / 2].x) * m);
+              out[h * D + 128] = narrow<F16>((h & 1 ? o1[h / 2].y : o1[h / 2].x) * m);
             }
           }
-          if (warp == 0 && lane < p.group) {
-            const float l2 = l == 0.f ? -INFINITY : m_lane + log2f(l);
+          if ((warp & 3) == 0 && lane < heads) {
+            const float l2 = l == 0.f ? -INFINITY : mref_lane + log2f(l);
             if (p.lse) p.lse[hq + lane] = l2 * 0.69314718055994531f;
             if (p.lse2) p.lse2[hq + lane] = l2;
           }
         } else {
           // slot 2 i: the pair that run i begins with; 2 i + 1: the one it ends with
-          const int64_t slot = 2 * (int64_t)blockIdx.x + (pair == pair0 ? 0 : 1);
-          float* po = p.part_o + slot * p.group * D + tid;
+          const int64_t head0 = (2 * (int64_t)blockIdx.x + (pair == pair0 ? 0 : 1)) * p.group + team * GH;
+          float* po = p.part_o + head0 * D + e_tid;
 #pragma unroll
-          for (int h = 0; h < HG; ++h)
-            if (h < p.group) {
-              po[h * D] = o0[h];
-              po[h * D + 128] = o1[h];
+          for (int h = 0; h < GH; ++h)
+            if (h < heads) {
+              po[h * D] = h & 1 ? o0[h / 2].y : o0[h / 2].x;
+              po[h * D + 128] = h & 1 ? o1[h / 2].y : o1[h / 2].x;
             }
-          if (warp == 0 && lane < p.group) {
-            p.part_ml[(slot * p.group + lane) * 2] = m_lane;
-            p.part_ml[(slot * p.group + lane) * 2 + 1] = l;
+          if ((warp & 3) == 0 && lane < heads) {
+            p.part_ml[(head0 + lane) * 2] = l == 0.f ? -INFINITY : mref_lane;
+            p.part_ml[(head0 + lane) * 2 + 1] = l;
           }
         }
       }
@@ -747,7 +869,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, C::TMEM);
+  if (warp == 12) tmem_dealloc(tmem, C::TMEM);
 }
 
 // Merges the pieces of pairs cut by the end of a run: one warp per (cut, head).

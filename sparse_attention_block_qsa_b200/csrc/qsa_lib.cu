@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 
 #include "qsa.h"
 #include "decode.cuh"
@@ -145,31 +146,18 @@ qsa_status_t device_info(int* sms) {
         {reinterpret_cast<const void*>(qsa::prefill::prefill_kernel<false>), qsa::prefill::SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::prefill::prefill_kernel<true>), qsa::prefill::SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::attn::attn_kernel), qsa::attn::SMEM_BYTES},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>), qsa::attn8::Cfg<false, 8>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 12>), qsa::attn8::Cfg<false, 12>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 16>), qsa::attn8::Cfg<false, 16>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>), qsa::attn8::Cfg<true, 8>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>), qsa::attn8::Cfg<true, 12>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 16>), qsa::attn8::Cfg<true, 16>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 4>), qsa::attn8::Cfg<false>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 6>), qsa::attn8::Cfg<false>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>), qsa::attn8::Cfg<false>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 4>), qsa::attn8::Cfg<true>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 6>), qsa::attn8::Cfg<true>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>), qsa::attn8::Cfg<true>::SMEM},
         {reinterpret_cast<const void*>(qsa::topk::topk_rows_kernel), qsa::topk::ROWS_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_pipe_kernel), qsa::topk::PIPE_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_filter_kernel), qsa::topk::TP_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_list_kernel),
          qsa::topk::TP_LIST_WARPS * qsa::topk::tp_list_warp_bytes(qsa::topk::MAX_W)},
     };
-    // These kernels share their launch registers out by setmaxnreg: fewer than they count on would never do.
-    for (const void* fn : {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>),
-                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 12>),
-                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 16>),
-                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>),
-                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>)}) {
-      cudaFuncAttributes a = {};
-      e = cudaFuncGetAttributes(&a, fn);
-      if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
-      if (a.numRegs < qsa::attn8::REGS_LAUNCH)
-        return fail(QSA_ERR_UNSUPPORTED, "attention over the 8-bit cache was built with %d registers a thread; %d needed",
-                    a.numRegs, qsa::attn8::REGS_LAUNCH);
-    }
     for (auto& k : kernels) {
       e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.bytes);
       if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -446,9 +434,9 @@ void attn_splits(int64_t T, int32_t Hkv, int32_t width, int32_t* splits, int32_t
   *cps = (int32_t)per;
 }
 
-// Runs of the 8-bit cache's attention: two CTAs on each of 148 SMs (a number of
+// Runs of the 8-bit cache's attention: one CTA on each of 148 SMs (a number of
 // its own, so that the workspace depends on the shapes only), no more than tiles.
-constexpr int64_t kAttn8Runs = 296;
+constexpr int64_t kAttn8Runs = 148;
 
 int64_t attn8_tiles(int32_t width) { return std::max<int64_t>(1, ((int64_t)width + qsa::attn8::TILE - 1) / qsa::attn8::TILE); }
 
@@ -1261,10 +1249,9 @@ size_t qsa_sparse_attention_fp8_workspace_size(int64_t T, int32_t Hq, int32_t Hk
 }
 
 extern "C++" {
-template <bool F16, int HG>
+template <bool F16, int GH>
 static void launch_attn8(const qsa::attn8::Params& p, cudaStream_t s) {
-  using C = qsa::attn8::Cfg<F16, HG>;
-  qsa::attn8::attn_fp8_kernel<F16, HG><<<(unsigned)p.ctas, qsa::attn8::THREADS, C::SMEM, s>>>(p);
+  qsa::attn8::attn_fp8_kernel<F16, GH><<<(unsigned)p.ctas, qsa::attn8::THREADS, qsa::attn8::Cfg<F16>::SMEM, s>>>(p);
   const int64_t warps = (int64_t)(p.ctas - 1) * p.group;   // one per cut between runs and head
   if (warps > 0 && (p.total % p.ctas != 0 || (p.total / p.ctas) % p.tiles != 0))
     qsa::attn8::combine_fp8_kernel<F16><<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(p);
@@ -1327,6 +1314,16 @@ static qsa_status_t attention_fp8_common(
   if (!workspace || workspace_bytes < w.total)
     return fail(QSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace_bytes, w.total);
   if (!aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  // The cache as one matrix of 256-byte rows, `pitch` bytes apart: every (page, token, head) row is one of them.
+  const int64_t page_stride = num_pages > 1 ? kv_page_stride : 0, row_stride = page_size > 1 ? kv_row_stride : 0,
+                head_stride = Hkv > 1 ? kv_head_stride : 0;
+  int64_t pitch = std::gcd(std::gcd(page_stride, row_stride), head_stride);
+  if (pitch == 0) pitch = D;
+  const int64_t rows =
+      ((num_pages - 1) * page_stride + (page_size - 1) * row_stride + (Hkv - 1) * head_stride) / pitch + 1;
+  if (rows >= INT32_MAX)
+    return fail(QSA_ERR_UNSUPPORTED, "the cache spans %lld rows of %lld bytes (the strides' greatest common divisor); "
+                "2^31 - 2 supported", (long long)rows, (long long)pitch);
   if (want_w && T * width > (int64_t)INT32_MAX * 256) return fail(QSA_ERR_UNSUPPORTED, "too many entries for one launch");
   int sms = 0;
   st = device_info(&sms);
@@ -1347,9 +1344,10 @@ static qsa_status_t attention_fp8_common(
   p.page_size = page_size;
   p.by_page = fast_div((uint32_t)page_size);
   p.by_block = fast_div((uint32_t)block_tokens);
-  p.kv_page_stride = kv_page_stride;
-  p.kv_row_stride = kv_row_stride;
-  p.kv_head_stride = kv_head_stride;
+  p.page_rows = (int32_t)(page_stride / pitch);
+  p.token_rows = (int32_t)(row_stride / pitch);
+  p.head_rows = (int32_t)(head_stride / pitch);
+  p.pitch = pitch;
   p.sc_page_stride = sc_page_stride;
   p.sc_block_stride = sc_block_stride;
   p.page_table = page_table;
@@ -1363,9 +1361,10 @@ static qsa_status_t attention_fp8_common(
   p.width = width;
   p.T = T;
   p.tiles = (int32_t)attn8_tiles(width1);
-  p.total = T * Hkv * p.tiles;
-  const int HG = p.group <= 8 ? 8 : p.group <= 12 ? 12 : 16;
-  p.ctas = (int32_t)std::min<int64_t>(p.total, f16 && HG == 16 ? kAttn8Runs / 2 : kAttn8Runs);
+  p.total = T * Hkv * (int64_t)p.tiles;
+  if (T * Hkv > INT32_MAX || p.total / kAttn8Runs * 2 >= INT32_MAX / 4)
+    return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
+  p.ctas = (int32_t)std::min(p.total, kAttn8Runs);
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
@@ -1378,14 +1377,15 @@ static qsa_status_t attention_fp8_common(
   p.weights = want_w ? weights : nullptr;
   p.w_stride = T > 1 ? weights_stride : width;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // query heads of a team: half of the group, in pairs
   if (f16) {
-    if (HG == 8) launch_attn8<true, 8>(p, s);
-    else if (HG == 12) launch_attn8<true, 12>(p, s);
-    else launch_attn8<true, 16>(p, s);
+    if (p.group <= 8) launch_attn8<true, 4>(p, s);
+    else if (p.group <= 12) launch_attn8<true, 6>(p, s);
+    else launch_attn8<true, 8>(p, s);
   } else {
-    if (HG == 8) launch_attn8<false, 8>(p, s);
-    else if (HG == 12) launch_attn8<false, 12>(p, s);
-    else launch_attn8<false, 16>(p, s);
+    if (p.group <= 8) launch_attn8<false, 4>(p, s);
+    else if (p.group <= 12) launch_attn8<false, 6>(p, s);
+    else launch_attn8<false, 8>(p, s);
   }
   if (want_w) weights_kernel<<<(unsigned)((T * width + 255) / 256), 256, 0, s>>>(p);
   return launch_status("8-bit cache attention kernels");
