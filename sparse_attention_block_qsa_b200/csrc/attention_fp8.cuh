@@ -26,22 +26,21 @@
 //    for the output); each tile's O^T is read back from TMEM and added.
 //
 // Work is the list of (row, KV head, 128-entry tile) triples in order; every CTA
-// takes an equal contiguous run of it (one CTA per SM), so any batch fills the
+// takes an equal contiguous run of it (two CTAs per SM), so any batch fills the
 // GPU to one tile.  A run may begin and end inside a row's list: such pieces go
 // to the workspace and combine_fp8_kernel merges them.  Inside a CTA
-//  * warps 8-11 look entries up (list, page table) and gather their K and V rows
-//    with 16-byte cp.async into six 32 KB buffers that K and V tiles take in
+//  * warps 4-7 look entries up (list, page table) and gather their K and V rows
+//    with 16-byte cp.async into three 32 KB buffers that K and V tiles take in
 //    turn.  (TMA gathers are no match here: measured 10.7 cycles a 128-byte row
 //    and SM for tile::gather4 and 27 a row for row-wise bulk copies, against 64
 //    bytes a cycle and SM, 19 TB/s out of L2, for cp.async);
-//  * warp 12 issues the MMAs, whichever product has its operands: S runs up to
-//    four tiles ahead of the softmax;
-//  * warps 14 and 15 split each new row's queries;
-//  * warps 0-3 and 4-7 run the softmax, each warpgroup for half of the query
-//    heads (thread = entry, then feature).  Scores are taken relative to a
-//    reference maximum that moves only when a tile exceeds it by 2^4 (or its
-//    v_scale by 1.75): until then a tile needs no reduction, only a vote, and its
-//    output product adds up in TMEM.
+//  * warp 8 issues the MMAs, whichever product has its operands: S runs up to
+//    S_BUFS tiles ahead of the softmax;
+//  * warps 9-11 split each new row's queries;
+//  * warps 0-3 run the softmax (thread = entry, then feature).  Scores are taken
+//    relative to a reference maximum that moves only when a tile exceeds it by
+//    2^3 (or its v_scale by a factor of 3.5): until then a tile needs no reduction,
+//    only a vote, and its output product adds up in TMEM.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -55,36 +54,44 @@ namespace attn8 {
 
 constexpr int D = 256;
 constexpr int TILE = 128;              // list entries per tile (UMMA M)
-constexpr int TEAM = 128;              // threads of a softmax warpgroup: entry (scores), feature (output)
-constexpr int SOFT = 2 * TEAM;
+constexpr int SOFT = 128;              // softmax threads: entry (scores), feature (output)
 constexpr int PROD = 128;              // gathering threads
 constexpr int THREADS = SOFT + PROD + 128;   // the last warpgroup: MMA issue, queries
+// Registers a thread: 384 threads twice on an SM leave 80 each at launch; the
+// warpgroups then share them out (the same sum of 240).
+constexpr int REGS_LAUNCH = 80, REGS_SOFT = 152, REGS_PROD = 48, REGS_REST = 40;
+static_assert(REGS_SOFT + REGS_PROD + REGS_REST <= 3 * REGS_LAUNCH, "setmaxnreg would wait for ever");
 // A probability is at most 2^REF_SLACK times the reference and v_scale at most
 // V_SLACK times its own; times P_UNIT that is E4M3's largest value.
-constexpr float REF_SLACK = 4.f, V_SLACK = 1.75f, P_UNIT = 16.f;
+constexpr float REF_SLACK = 3.f, V_SLACK = 3.5f, P_UNIT = 16.f;
 constexpr int MAX_GROUP = 16;          // query heads per KV head
 constexpr int PT = 3;                  // E4M3 terms of a probability
-constexpr int BUFS = 6;                // K and V tiles held
-constexpr int S_BUFS = 4;              // score tiles held in TMEM
+constexpr int BUFS = 3;
 constexpr int HALF_BYTES = TILE * 128;       // 128 features of every entry
 constexpr int BUF_BYTES = 2 * HALF_BYTES;
-constexpr int QC_SLOTS = 8;            // rows whose head factors are held: S_BUFS ahead and the current one fit
-constexpr int TH = 8;                  // columns a team has for a term; it fills GH (4, 6 or 8) of them
+constexpr int QC_SLOTS = 8;            // rows whose head factors are held: the current one and S_BUFS ahead fit
+constexpr int Q_WARPS = 3;
 
-// Sizes of one instance.
-template <bool F16>
+// Sizes of one instance: 16-bit type and query heads held per KV head.
+template <bool F16, int HG>
 struct Cfg {
-  static constexpr int QT = F16 ? 3 : 2;          // E4M3 terms of a query element
-  static constexpr int QN = 2 * QT * TH;          // score columns: [team][term][TH heads]
-  static constexpr int PN = 2 * PT * TH;          // output columns, laid out the same way
-  static constexpr uint32_t TMEM = S_BUFS * QN + 2 * PN <= 256 ? 256 : 512;
-  static constexpr int Q_BYTES = QN * D;
+  static constexpr int QT = F16 ? 3 : 2;                          // E4M3 terms of a query element
+  static constexpr int QCOLS = QT * HG, QN = (QCOLS + 15) / 16 * 16, QROWS = (QCOLS + 7) / 8 * 8;
+  static constexpr int PCOLS = PT * HG, PN = (PCOLS + 15) / 16 * 16;
+  static constexpr int S_BUFS = F16 ? 3 : 4;                      // score tiles held in TMEM
+  static constexpr uint32_t TMEM = 256;                           // columns; two CTAs share 512
+  static_assert(S_BUFS * QN + 2 * PN <= TMEM, "TMEM columns");
+  static constexpr int Q_BYTES = QROWS * D;
   static constexpr int P_BYTES = PN * TILE;
-  static constexpr int BARS = 2 * BUFS + 2 * S_BUFS + 4 + 3;
-  static constexpr size_t SMEM = BUFS * BUF_BYTES + Q_BYTES + 2 * P_BYTES + BARS * 8 + 8 * (TH + 1) * 4 +
-                                 QC_SLOTS * 2 * TH * 4 + 16;
+  static constexpr int BARS = 2 * BUFS + 2 * S_BUFS + 5;
+  // Scales of two tiles in shared memory, copied with the K rows; where there is no room (fp16, 12 heads) the
+  // softmax threads look their entries up themselves.
+  static constexpr bool RING = !(F16 && HG == 12);
+  static constexpr int RING_BYTES = RING ? 2 * TILE * 8 : 0;
+  static constexpr size_t SMEM =
+      BUFS * BUF_BYTES + Q_BYTES + P_BYTES + RING_BYTES + BARS * 8 + 4 * 17 * 4 + QC_SLOTS * HG * 4 + 16;
+  static constexpr int RESIDENT = 2 * (SMEM + 1024) <= 233472 ? 2 : 1;   // CTAs per SM
 };
-static_assert(Cfg<true>::SMEM <= 232448, "shared memory per block");
 
 // n / d for 0 <= n < 2^31 as a product and a shift.
 struct FastDiv {
@@ -213,6 +220,9 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 2^-inf = 0
 
 // Arrives on bar once this thread's cp.async copies so far have landed; the
 // barrier counts this arrival like any other.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -366,26 +376,40 @@ struct Feed {
   }
 };
 
-template <bool F16, int GH>
-__global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
-  using C = Cfg<F16>;
-  constexpr int QT = C::QT, QN = C::QN, PN = C::PN;
-  constexpr uint32_t Q_HALF = QN * 128;
+__device__ __forceinline__ int64_t scale_index(const Params& p, int page, int in_page, int g) {
+  return (int64_t)page * p.sc_page_stride + (int64_t)divide(in_page, p.by_block) * p.sc_block_stride + g;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <bool F16, int HG>
+__global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_kernel(const Params p) {
+  using C = Cfg<F16, HG>;
+  constexpr int QT = C::QT, QN = C::QN, PN = C::PN, S_BUFS = C::S_BUFS;
+  constexpr uint32_t Q_HALF = C::QROWS * 128;
   constexpr uint32_t IDESC_S = idesc_e4m3(TILE, QN, false, false);
   constexpr uint32_t IDESC_O = idesc_e4m3(128, PN, true, true);
   extern __shared__ __align__(1024) uint8_t smem8[];   // the swizzle repeats every 1024 bytes
   uint8_t* buf_s = smem8;
-  uint8_t* q_s = buf_s + BUFS * BUF_BYTES;             // [half][QN][128 bytes], swizzled
-  uint8_t* p_s = q_s + C::Q_BYTES;                     // [2][16 columns][entry][16 bytes]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(p_s + 2 * C::P_BYTES);
+  uint8_t* q_s = buf_s + BUFS * BUF_BYTES;             // [half][QROWS][128 bytes], swizzled; row = term * HG + head
+  uint8_t* p_s = q_s + C::Q_BYTES;                     // [16 columns][entry][16 bytes]; column = term * HG + head
+  float* sc_s = reinterpret_cast<float*>(p_s + C::P_BYTES);   // [2][K, V][TILE] scales, 0 for unseen entries
+  uint64_t* bars = reinterpret_cast<uint64_t*>(p_s + C::P_BYTES + C::RING_BYTES);
   uint64_t *kv_full = bars, *kv_empty = kv_full + BUFS, *s_full = kv_empty + BUFS, *s_empty = s_full + S_BUFS,
-           *p_full = s_empty + S_BUFS, *o_full = p_full + 2, *q_full = o_full + 2, *q_empty = q_full + 1,
+           *p_full = s_empty + S_BUFS, *o_full = p_full + 1, *q_full = o_full + 1, *q_empty = q_full + 1,
            *drained = q_empty + 1;
-  float* red_s = reinterpret_cast<float*>(bars + C::BARS);  // [8 warps][TH + 1]: tile maxima by head, v_scale
-  float* qc_s = red_s + 8 * (TH + 1);                  // [QC_SLOTS][team][TH]: a head's power of two times scale * log2(e)
-  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(qc_s + QC_SLOTS * 2 * TH);
+  float* red_s = reinterpret_cast<float*>(bars + C::BARS);  // [4 warps][17]: tile maxima by head, v_scale
+  float* qc_s = red_s + 4 * 17;                        // [QC_SLOTS][HG]: a head's power of two times scale * log2(e)
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(qc_s + QC_SLOTS * HG);
   volatile int* abort = reinterpret_cast<int*>(tmem_s + 1);
-  volatile int* add_s = abort + 1;                     // [2] whether an output product adds to what TMEM holds
+  volatile int* add_s = abort + 1;                     // whether the next output product adds to what TMEM holds
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t u0 = run_begin(p, blockIdx.x);
@@ -393,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
   const int pair0 = (int)(u0 / p.tiles);
   const int tile0 = (int)(u0 - (int64_t)pair0 * p.tiles);
 
-  if (warp == 12) tmem_alloc(tmem_s, C::TMEM);
+  if (warp == 8) tmem_alloc(tmem_s, C::TMEM);
   if (tid == 0) {
     for (int i = 0; i < BUFS; ++i) {
       mbar_init(&kv_full[i], PROD);
@@ -403,11 +427,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
       mbar_init(&s_full[i], 2);
       mbar_init(&s_empty[i], SOFT);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_full[i], SOFT);
-      mbar_init(&o_full[i], 1);
-    }
-    mbar_init(q_full, 64);
+    mbar_init(p_full, SOFT);
+    mbar_init(o_full, 1);
+    mbar_init(q_full, Q_WARPS * 32);
     mbar_init(q_empty, 1);
     mbar_init(drained, 1);
     fence_mbar_init();
@@ -417,26 +439,32 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_s;
-  const uint32_t tm_o = tmem + S_BUFS * QN;            // two halves of PN columns
+  const uint32_t tm_o = tmem + S_BUFS * QN;                 // two halves of PN columns
   // A wait that runs out sets *abort.  Gathering and issuing warps then leave; the softmax warps go on through
-  // their tiles without waiting, so that their barriers are always met.
+  // their tiles without waiting, so that their barrier is always met.
   auto gone = [&]() {
     record_device_error(QSA_DEVERR_WAIT_TIMEOUT);
     *abort = 1;
   };
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 4 && warp < 8) {
     // ---------------------------------------------------------------- gather
-    const int w = warp - 8;
+    if constexpr (C::RESIDENT > 1) regs_shrink<REGS_PROD>();
+    const int w = warp - 4;
     const int u = lane & 15, row2 = lane >> 4;         // 16 lanes a row, two rows per instruction
     Feed<1> f;
     f.start(p, pair0, tile0, n, 32 * w + lane, lane);
     // rows of the warp's 32 entries into buffer item % BUFS
-    auto gather = [&](const uint8_t* base, int row, int item) -> bool {
+    auto gather = [&](const uint8_t* base, int row, int item, int64_t scale_at) -> bool {
       const int b = item % BUFS;
       if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[b], (uint32_t)((item / BUFS) & 1) ^ 1, abort))) return false;
       const uint32_t dst = smem_addr(buf_s + b * BUF_BYTES) + (u >> 3) * HALF_BYTES + (32 * w + row2) * 128;
       const uint8_t* src = base + u * 16;
+      if (C::RING && (item & 1) == 0) {                // the tile's scales land with its K rows
+        const uint32_t at = smem_addr(sc_s + (item >> 1 & 1) * 2 * TILE + 32 * w + lane);
+        cp_async4(at, p.k_scale + scale_at, row >= 0);
+        cp_async4(at + TILE * 4, p.v_scale + scale_at, row >= 0);
+      }
       int rr[16];                                      // all the look-ups before the copies
 #pragma unroll
       for (int i = 0; i < 16; ++i) rr[i] = __shfl_sync(0xffffffffu, row, 2 * i + row2);
@@ -450,16 +478,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
     for (int k = 0; k < n; ++k) {
       int page[1], j[1], g;
       f.next(p, page, j, g);
-      const int row = page[0] < 0 ? -1
-                                  : page[0] * p.page_rows +
-                                        (j[0] - divide(j[0], p.by_page) * p.page_size) * p.token_rows + g * p.head_rows;
-      if (!gather(p.k, row, 2 * k) || !gather(p.v, row, 2 * k + 1)) {
+      const int in_page = j[0] - divide(j[0], p.by_page) * p.page_size;
+      const int row = page[0] < 0 ? -1 : page[0] * p.page_rows + in_page * p.token_rows + g * p.head_rows;
+      const int64_t at = C::RING && row >= 0 ? scale_index(p, page[0], in_page, g) : 0;
+      if (!gather(p.k, row, 2 * k, at) || !gather(p.v, row, 2 * k + 1, 0)) {
         gone();
         break;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 12) {
+  } else if (warp == 8) {
+    if constexpr (C::RESIDENT > 1) regs_shrink<REGS_REST>();
     // ---------------------------------------------------------------- MMA issue
     // The whole warp goes round, so that descriptors stay in uniform registers; one lane issues.
     const uint64_t q_desc = umma_desc_sw128(smem_addr(q_s));
@@ -468,28 +497,29 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
     int ks = 0, ko = 0;                                // next tile of either product
     int kb = 0, vb = 1;                                // their buffers
     uint32_t kp = 0, vp = 0;                           // and those buffers' phases
+    int sb = 0;                                        // score buffer of ks and its phase
+    uint32_t sp = 0;
     int tile = tile0, nth = 0;                         // of S: tile in its pair, pairs begun
     bool fresh = true;
     uint64_t since = global_timer_ns();
     uint32_t idle = 0;
     while (ko < n) {
       bool did = false;
-      if (ko < ks && __all_sync(0xffffffffu, mbar_test(&p_full[ko & 1], (uint32_t)(ko >> 1) & 1) &&
+      if (ko < ks && __all_sync(0xffffffffu, mbar_test(p_full, (uint32_t)ko & 1) &&
                                                  mbar_test(&kv_full[vb], vp))) {
         fence_proxy_async_smem();                      // the cp.async writes, before the tensor core reads them
         tc_fence_after();
-        const bool add = add_s[ko & 1] != 0;
+        const bool add = *add_s != 0;
         const uint64_t vd = kv_desc + (uint32_t)(vb * (BUF_BYTES >> 4));
-        const uint64_t pd = p_desc + (uint32_t)((ko & 1) * (C::P_BYTES >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              mma_e4m3(tm_o + hf * PN, vd + hf * (HALF_BYTES >> 4) + s * (32 * 128 >> 4), pd + s * (32 * 16 >> 4),
+              mma_e4m3(tm_o + hf * PN, vd + hf * (HALF_BYTES >> 4) + s * (32 * 128 >> 4), p_desc + s * (32 * 16 >> 4),
                        IDESC_O, add || s > 0);
           umma_commit(&kv_empty[vb]);
-          umma_commit(&o_full[ko & 1]);
+          umma_commit(o_full);
         }
         __syncwarp();
         ++ko;
@@ -502,12 +532,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
       }
       if (ks < n && ks < ko + S_BUFS &&
           __all_sync(0xffffffffu, mbar_test(&kv_full[kb], kp) &&
-                                      mbar_test(&s_empty[ks % S_BUFS], (uint32_t)((ks / S_BUFS) & 1) ^ 1) &&
+                                      mbar_test(&s_empty[sb], sp ^ 1) &&
                                       (!fresh || mbar_test(q_full, (uint32_t)nth & 1)))) {
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t kd = kv_desc + (uint32_t)(kb * (BUF_BYTES >> 4));
-        const uint32_t d = tmem + (uint32_t)(ks % S_BUFS) * QN;
+        const uint32_t d = tmem + (uint32_t)sb * QN;
         const bool last = tile + 1 == p.tiles;
         if (elect_one()) {
 #pragma unroll
@@ -515,8 +545,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
             mma_e4m3(d, kd + (s >> 2) * (HALF_BYTES >> 4) + (s & 3) * 2, q_desc + (s >> 2) * (Q_HALF >> 4) + (s & 3) * 2,
                      IDESC_S, s > 0);
           umma_commit(&kv_empty[kb]);
-          mbar_arrive(&s_full[ks % S_BUFS]);           // hands on what q_full published (the head factors)
-          umma_commit(&s_full[ks % S_BUFS]);
+          mbar_arrive(&s_full[sb]);                  // hands on what q_full published (the head factors)
+          umma_commit(&s_full[sb]);
           if (last) umma_commit(q_empty);
         }
         __syncwarp();
@@ -524,6 +554,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
         tile = last ? 0 : tile + 1;
         nth += last ? 1 : 0;
         ++ks;
+        if (++sb == S_BUFS) {
+          sb = 0;
+          sp ^= 1;
+        }
         kb += 2;
         if (kb >= BUFS) {
           kb -= BUFS;
@@ -544,91 +578,80 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
       }
     }
     __syncwarp();
-  } else if (warp >= 14) {
-    // ---------------------------------------------------------------- queries: warp w takes heads w, w + 2, ...
-    const int w = warp - 14;
+  } else if (warp > 8) {
+    if constexpr (C::RESIDENT > 1) regs_shrink<REGS_REST>();
+    // ---------------------------------------------------------------- queries: warp w takes heads w, w + 3, ...
+    const int w = warp - 9;
     const int pairs = (tile0 + n - 1) / p.tiles + 1;
     for (int nth = 0; nth < pairs; ++nth) {
       const int64_t t = (pair0 + nth) / p.Hkv;
       const int g = pair0 + nth - (int)t * p.Hkv;
       const uint16_t* q_row = p.q + t * p.q_st + (int64_t)g * p.group * p.q_sh + lane * 8;
-      uint4 x4[TH];                                    // read before the wait; columns past the group are zero
+      constexpr int PER = (HG + Q_WARPS - 1) / Q_WARPS;
+      uint4 x4[PER];                                   // read before the wait; heads past the group are zero
 #pragma unroll
-      for (int i = 0; i < TH; ++i) {
-        const int c = w + 2 * i, hh = c % TH, h = c / TH * GH + hh;
+      for (int i = 0; i < PER; ++i) {
+        const int h = w + Q_WARPS * i;
         x4[i] = make_uint4(0, 0, 0, 0);
-        if (hh < GH && h < p.group) x4[i] = __ldg(reinterpret_cast<const uint4*>(q_row + h * p.q_sh));
+        if (h < p.group) x4[i] = __ldg(reinterpret_cast<const uint4*>(q_row + h * p.q_sh));
       }
       if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (uint32_t)(nth & 1) ^ 1, abort))) {
         gone();
         break;
       }
 #pragma unroll
-      for (int i = 0; i < TH; ++i) {
-        const int c = w + 2 * i, hh = c % TH, h = c / TH * GH + hh;
+      for (int i = 0; i < PER; ++i) {
+        const int h = w + Q_WARPS * i;
+        if (h >= HG) break;
         const uint32_t w4[4] = {x4[i].x, x4[i].y, x4[i].z, x4[i].w};
-        float x[8];
-        float top = 0.f;
-        bool bad = false;
+        // the head's largest magnitude, as a 16-bit pattern (NaN and infinity sort above every number)
+        uint32_t top2 = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 v = widen2<F16>(w4[k]);
-          x[2 * k] = v.x;
-          x[2 * k + 1] = v.y;
-          top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-          bad = bad || !(fabsf(v.x) <= 3.4e38f) || !(fabsf(v.y) <= 3.4e38f);
-        }
-        top = warp_max(top);
-        bad = __any_sync(0xffffffffu, bad);
-        // the power of two that brings the largest element into [224, 448]: 448 = 1.75 * 2^8
-        const uint32_t tb = __float_as_uint(top);
-        int e = (int)(tb >> 23) - 127 - 8 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0);
-        e = max(e, -126);
-        const float inv1 = __uint_as_float((uint32_t)(127 + (-e) / 2) << 23);       // 2^(-e) in two factors:
-        const float inv2 = __uint_as_float((uint32_t)(127 + (-e) - (-e) / 2) << 23);  // one may leave fp32's range
-        uint32_t term[QT][2];
+        for (int k = 0; k < 4; ++k) top2 = __vmaxu2(top2, w4[k] & 0x7fff7fffu);
+        const uint32_t top16 = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
+        const bool bad = top16 >= (F16 ? 0x7c00u : 0x7f80u);
+        // the power of two that brings it into [224, 448]: 448 = 1.75 * 2^8
+        const uint32_t tb = __float_as_uint(widen2<F16>(top16).x);
+        const int e = max((int)(tb >> 23) - 127 - 8 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+        const float2 inv = both(bad ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - e) << 23));
+        float2 y[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float y[4];
-#pragma unroll
-          for (int m = 0; m < 4; ++m) y[m] = bad ? __uint_as_float(0x7fc00000u) : x[4 * k + m] * inv1 * inv2;
-#pragma unroll
-          for (int q = 0; q < QT; ++q) {
-            const uint32_t c0 = e4m3x2(y[0], y[1]), c1 = e4m3x2(y[2], y[3]);
-            term[q][k] = c0 | (c1 << 16);
-            const float2 f0 = e4m3x2_value(c0), f1 = e4m3x2_value(c1);
-            y[0] = (y[0] - f0.x) * 16.f;
-            y[1] = (y[1] - f0.y) * 16.f;
-            y[2] = (y[2] - f1.x) * 16.f;
-            y[3] = (y[3] - f1.y) * 16.f;
-          }
-        }
+        for (int k = 0; k < 4; ++k) y[k] = mul2(widen2<F16>(w4[k]), inv);
         const int un = lane >> 1;                      // 16-byte unit of the row
 #pragma unroll
         for (int q = 0; q < QT; ++q) {
-          const int nr = (c / TH) * (QT * TH) + q * TH + hh;
+          uint32_t code[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            code[k] = e4m3x2(y[k].x, y[k].y);
+            if (q + 1 < QT) y[k] = fma2(e4m3x2_value(code[k]), both(-16.f), mul2(y[k], both(16.f)));
+          }
+          const int nr = q * HG + h;
           uint8_t* dst = q_s + (un >> 3) * Q_HALF + nr * 128 + (((un & 7) ^ (nr & 7)) << 4) + (lane & 1) * 8;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(term[q][0], term[q][1]);
+          *reinterpret_cast<uint2*>(dst) = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
         }
-        if (lane == 0) qc_s[(nth % QC_SLOTS) * 2 * TH + c] = hh < GH && h < p.group ? ldexpf(p.scale_log2, e) : 0.f;
+        if (lane == 0)
+          qc_s[(nth % QC_SLOTS) * HG + h] =
+              h < p.group ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : 0.f;
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     }
-  } else if (warp < 8) {
-    // ---------------------------------------------------------------- softmax: a team for each half of the heads
-    const int team = warp >> 2, e_tid = tid & (TEAM - 1);
-    const uint32_t tm_lane = (uint32_t)((warp & 3) * 32) << 16;
-    const int heads = min(GH, p.group - team * GH);    // of this team (may be below 1: nothing to write)
+  } else {
+    // ---------------------------------------------------------------- softmax
+    if constexpr (C::RESIDENT > 1) regs_grow<REGS_SOFT>();
+    const uint32_t tm_lane = (uint32_t)(warp * 32) << 16;
     Feed<1> f;
-    f.start(p, pair0, tile0, n, e_tid, lane);
-    // heads 2 i, 2 i + 1: sums over this thread's entries; features e_tid and 128 + e_tid
-    float2 l_run[GH / 2], o0[GH / 2], o1[GH / 2];
-    float mref[GH];                                    // same in every thread of the team
+    if constexpr (!C::RING) f.start(p, pair0, tile0, n, tid, lane);
+    // heads 2 i, 2 i + 1: sums over this thread's entries; features tid and 128 + tid
+    float2 l_run[HG / 2], o0[HG / 2], o1[HG / 2];
+    float mref[HG];                                    // same in every thread
     float vref = 0.f, vinv = 0.f;
     bool set = false;                                  // mref holds maxima: a tile had a visible entry
     bool add = false;                                  // TMEM holds output of this pair that o0, o1 lack
     int pair = pair0, tile = tile0, nth = 0;
+    int sb = 0;                                        // score buffer and its phase
+    uint32_t sp = 0;
     bool fresh = true;
     // scales of the next tile's entry: loaded one tile ahead
     float ks_nx = 0.f, vs_nx = 0.f;
@@ -638,111 +661,114 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
       f.next(p, page, j, g);
       seen_nx = page[0] >= 0;
       const int in_page = j[0] - divide(j[0], p.by_page) * p.page_size;
-      const int64_t at = seen_nx ? (int64_t)page[0] * p.sc_page_stride +
-                                       (int64_t)divide(in_page, p.by_block) * p.sc_block_stride + g
-                                 : 0;
+      const int64_t at = seen_nx ? scale_index(p, page[0], in_page, g) : 0;
       ks_nx = __ldg(p.k_scale + at);                   // element 0 always exists; unseen entries do not use it
       vs_nx = __ldg(p.v_scale + at);
     };
-    scales();
-    auto output_done = [&](int k) {                    // tile k's product is in TMEM, its P free
-      if (!mbar_wait(&o_full[k & 1], (uint32_t)(k >> 1) & 1, abort)) gone();
+    if constexpr (!C::RING) scales();
+    auto output_done = [&](int k) {                // tile k's product is in TMEM, its P free
+      if (!mbar_wait(o_full, (uint32_t)k & 1, abort)) gone();
       tc_fence_after();
     };
     auto take_output = [&]() {                         // o += what TMEM holds
       const float2 unit = both(vref * (1.f / P_UNIT));
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float d[PT * TH];
-        tmem_ld(tm_o + tm_lane + hf * PN + team * PT * TH, d);
+        float d[(C::PCOLS + 7) / 8 * 8];
+        tmem_ld(tm_o + tm_lane + hf * PN, d);
         tmem_wait_ld();
         float2* o = hf == 0 ? o0 : o1;
 #pragma unroll
-        for (int i = 0; i < GH / 2; ++i) {
+        for (int i = 0; i < HG / 2; ++i) {
           float2 x = make_float2(d[2 * i], d[2 * i + 1]);
-          x = fma2(make_float2(d[TH + 2 * i], d[TH + 2 * i + 1]), both(1.f / 16.f), x);
-          x = fma2(make_float2(d[2 * TH + 2 * i], d[2 * TH + 2 * i + 1]), both(1.f / 256.f), x);
+          x = fma2(make_float2(d[HG + 2 * i], d[HG + 2 * i + 1]), both(1.f / 16.f), x);
+          x = fma2(make_float2(d[2 * HG + 2 * i], d[2 * HG + 2 * i + 1]), both(1.f / 256.f), x);
           o[i] = fma2(x, unit, o[i]);
         }
       }
     };
     for (int k = 0; k < n; ++k) {
-      const bool seen = seen_nx;
-      const float ks = ks_nx, vs = seen ? vs_nx : 0.f;
-      float2 x[GH / 2];                                // scores, then relative to mref, then probabilities
+      bool seen = seen_nx;
+      float ks = ks_nx, vs = seen ? vs_nx : 0.f;
+      float2 x[HG / 2];                                // scores, then relative to mref, then probabilities
       {
-        if (!mbar_wait(&s_full[k % S_BUFS], (uint32_t)(k / S_BUFS) & 1, abort)) gone();
+        if (!mbar_wait(&s_full[sb], sp, abort)) gone();
         tc_fence_after();
+        if constexpr (C::RING) {
+          const float* sc = sc_s + (k & 1) * 2 * TILE + tid;
+          ks = sc[0];
+          vs = sc[TILE];
+          seen = ks != 0.f;
+        }
         if (fresh) {
 #pragma unroll
-          for (int h = 0; h < GH; ++h) mref[h] = 0.f;
+          for (int h = 0; h < HG; ++h) mref[h] = 0.f;
 #pragma unroll
-          for (int i = 0; i < GH / 2; ++i) l_run[i] = o0[i] = o1[i] = make_float2(0.f, 0.f);
+          for (int i = 0; i < HG / 2; ++i) l_run[i] = o0[i] = o1[i] = make_float2(0.f, 0.f);
           vref = vinv = 0.f;
           add = set = false;
         }
-        const float2* qc = reinterpret_cast<const float2*>(qc_s + ((nth % QC_SLOTS) * 2 + team) * TH);
-        float d[QT * TH];
-        tmem_ld(tmem + tm_lane + (uint32_t)(k % S_BUFS) * QN + team * QT * TH, d);
+        const float2* qc = reinterpret_cast<const float2*>(qc_s + (nth % QC_SLOTS) * HG);
+        float d[(C::QCOLS + 7) / 8 * 8];
+        tmem_ld(tmem + tm_lane + (uint32_t)sb * QN, d);
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive(&s_empty[k % S_BUFS]);
+        mbar_arrive(&s_empty[sb]);
+        if (++sb == S_BUFS) {
+          sb = 0;
+          sp ^= 1;
+        }
 #pragma unroll
-        for (int i = 0; i < GH / 2; ++i) {
-          x[i] = fma2(make_float2(d[TH + 2 * i], d[TH + 2 * i + 1]), both(1.f / 16.f), make_float2(d[2 * i], d[2 * i + 1]));
+        for (int i = 0; i < HG / 2; ++i) {
+          x[i] = fma2(make_float2(d[HG + 2 * i], d[HG + 2 * i + 1]), both(1.f / 16.f), make_float2(d[2 * i], d[2 * i + 1]));
           if (QT > 2)
-            x[i] = fma2(make_float2(d[(QT - 1) * TH + 2 * i], d[(QT - 1) * TH + 2 * i + 1]), both(1.f / 256.f), x[i]);
+            x[i] = fma2(make_float2(d[(QT - 1) * HG + 2 * i], d[(QT - 1) * HG + 2 * i + 1]), both(1.f / 256.f), x[i]);
           x[i] = mul2(x[i], mul2(qc[i], both(ks)));
           if (!seen) x[i] = make_float2(-INFINITY, -INFINITY);
         }
       }
       if (p.part_s) {
-        const int e = tile * TILE + e_tid;
+        const int e = tile * TILE + tid;
         if (e < p.width) {
-          float* dst = p.part_s + ((int64_t)pair * p.width + e) * p.group + team * GH;
+          float* dst = p.part_s + ((int64_t)pair * p.width + e) * p.group;
 #pragma unroll
-          for (int h = 0; h < GH; ++h)
-            if (h < heads) dst[h] = h & 1 ? x[h / 2].y : x[h / 2].x;
+          for (int h = 0; h < HG; ++h)
+            if (h < p.group) dst[h] = h & 1 ? x[h / 2].y : x[h / 2].x;
         }
       }
       float over = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < GH / 2; ++i) {
+      for (int i = 0; i < HG / 2; ++i) {
         x[i] = add2(x[i], make_float2(-mref[2 * i], -mref[2 * i + 1]));
         over = fmaxf(over, fmaxf(x[i].x, x[i].y));
       }
-      // one vote for both teams: whether an output product adds is common to all columns
       if (barrier_any(1, SOFT, !set || over > REF_SLACK || vs > V_SLACK * vref)) {
         // ---- new references: the tile's maxima where they are larger
         float mine = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < GH; ++h) {
+        for (int h = 0; h < HG; ++h) {
           const float wm = warp_max((h & 1 ? x[h / 2].y : x[h / 2].x) + mref[h]);
           if (lane == h) mine = wm;
         }
         const float vm = warp_max(vs);
-        if (lane == TH) mine = vm;
-        if (lane <= TH) red_s[warp * (TH + 1) + lane] = mine;
-        named_barrier_sync(2 + team, TEAM);
-        const float* red = red_s + team * 4 * (TH + 1);
+        if (lane == 16) mine = vm;
+        if (lane <= 16) red_s[warp * 17 + lane] = mine;
+        named_barrier_sync(2, SOFT);
         if (add) {
           output_done(k - 1);
           take_output();
           add = false;
         }
-        auto of_team = [&](int c) {
-          return fmaxf(fmaxf(red[c], red[TH + 1 + c]), fmaxf(red[2 * (TH + 1) + c], red[3 * (TH + 1) + c]));
-        };
-        vref = fmaxf(vref, of_team(TH));
+        vref = fmaxf(vref, fmaxf(fmaxf(red_s[16], red_s[33]), fmaxf(red_s[50], red_s[67])));
         vinv = vref > 0.f ? 1.f / vref : 0.f;
         bool any = false;
 #pragma unroll
-        for (int i = 0; i < GH / 2; ++i) {
+        for (int i = 0; i < HG / 2; ++i) {
           float a[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int h = 2 * i + e;
-            float m = of_team(h);
+            float m = fmaxf(fmaxf(red_s[h], red_s[17 + h]), fmaxf(red_s[34 + h], red_s[51 + h]));
             any = any || m > -INFINITY;
             if (set) m = fmaxf(m, mref[h]);
             if (!(m > -INFINITY)) m = 0.f;             // nothing visible yet (or only NaN)
@@ -756,50 +782,43 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
           o1[i] = mul2(o1[i], alpha);
         }
         set = set || any;
-        named_barrier_sync(2 + team, TEAM);            // red_s may be written again
+        named_barrier_sync(2, SOFT);                   // red_s may be written again
       }
-      scales();                                        // of tile k + 1
+      if constexpr (!C::RING) scales();                // of tile k + 1
       // ---- P times v_scale / vref as three E4M3 terms
       const float2 vn = both(vs * vinv * P_UNIT);
-      uint32_t w2[PT][2];
+      uint32_t w4[PN / 4];
 #pragma unroll
-      for (int q = 0; q < PT; ++q) w2[q][1] = 0;
-      float2 y[TH / 2];
+      for (int i = 0; i < PN / 4; ++i) w4[i] = 0;
 #pragma unroll
-      for (int i = 0; i < TH / 2; ++i) {
-        y[i] = make_float2(0.f, 0.f);
-        if (i < GH / 2) {
-          const float2 pr = make_float2(exp2_fast(x[i].x), exp2_fast(x[i].y));
-          l_run[i] = add2(l_run[i], pr);
-          y[i] = mul2(pr, vn);
+      for (int c = 0; c < HG / 4; ++c) {
+        float2 y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 pr = make_float2(exp2_fast(x[2 * c + e].x), exp2_fast(x[2 * c + e].y));
+          l_run[2 * c + e] = add2(l_run[2 * c + e], pr);
+          y[e] = mul2(pr, vn);
         }
-      }
 #pragma unroll
-      for (int q = 0; q < PT; ++q) {
-        uint32_t c[TH / 2];
-#pragma unroll
-        for (int i = 0; i < TH / 2; ++i) {
-          c[i] = 0;
-          if (i < GH / 2) {
-            c[i] = e4m3x2(y[i].x, y[i].y);
-            if (q + 1 < PT) y[i] = fma2(e4m3x2_value(c[i]), both(-16.f), mul2(y[i], both(16.f)));
+        for (int q = 0; q < PT; ++q) {
+          const uint32_t c0 = e4m3x2(y[0].x, y[0].y), c1 = e4m3x2(y[1].x, y[1].y);
+          w4[q * (HG / 4) + c] = c0 | (c1 << 16);
+          if (q + 1 < PT) {
+            y[0] = fma2(e4m3x2_value(c0), both(-16.f), mul2(y[0], both(16.f)));
+            y[1] = fma2(e4m3x2_value(c1), both(-16.f), mul2(y[1], both(16.f)));
           }
         }
-        w2[q][0] = c[0] | (c[1] << 16);
-        w2[q][1] = c[2] | (c[3] << 16);
       }
-      if (k > 1) output_done(k - 2);
-      uint8_t* dst = p_s + (k & 1) * C::P_BYTES + e_tid * 16;
+      if (k > 0) output_done(k - 1);
 #pragma unroll
-      for (int q = 0; q < PT; ++q) {
-        const int col = (team * PT + q) * TH;          // columns col .. col + 7: half of a 16-byte unit
-        *reinterpret_cast<uint2*>(dst + (col / 16) * (TILE * 16) + (col % 16)) = make_uint2(w2[q][0], w2[q][1]);
-      }
-      if (tid == 0) add_s[k & 1] = add ? 1 : 0;
+      for (int i = 0; i < PN / 16; ++i)
+        *reinterpret_cast<uint4*>(p_s + (i * TILE + tid) * 16) =
+            make_uint4(w4[4 * i], w4[4 * i + 1], w4[4 * i + 2], w4[4 * i + 3]);
+      if (tid == 0) *add_s = add ? 1 : 0;
       add = true;
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(&p_full[k & 1]);
+      mbar_arrive(p_full);
 
       fresh = ++tile == p.tiles;
       if (fresh || k + 1 == n) {
@@ -809,7 +828,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
         const bool whole = fresh && k + 1 >= p.tiles;
         float mine = 0.f, mref_lane = 0.f;             // of head `lane`
 #pragma unroll
-        for (int h = 0; h < GH; ++h) {
+        for (int h = 0; h < HG; ++h) {
           float l = h & 1 ? l_run[h / 2].y : l_run[h / 2].x;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -818,45 +837,44 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
             mref_lane = mref[h];
           }
         }
-        if (lane < TH) red_s[warp * (TH + 1) + lane] = mine;
-        named_barrier_sync(2 + team, TEAM);
-        const int at = lane & (TH - 1);
-        const float* red = red_s + team * 4 * (TH + 1) + at;
-        const float l = red[0] + red[TH + 1] + red[2 * (TH + 1)] + red[3 * (TH + 1)];
-        named_barrier_sync(2 + team, TEAM);
+        if (lane < 16) red_s[warp * 17 + lane] = mine;
+        named_barrier_sync(2, SOFT);
+        const int at = lane & 15;
+        const float l = red_s[at] + red_s[17 + at] + red_s[34 + at] + red_s[51 + at];
+        named_barrier_sync(2, SOFT);
         const int64_t t = pair / p.Hkv;
         const int g = pair - (int)t * p.Hkv;
         if (whole) {
           float mul = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
-          const int64_t hq = t * p.Hq + (int64_t)g * p.group + team * GH;
-          if (p.gate && at < heads) mul *= 1.f / (1.f + expf(-p.gate[hq + at]));
-          uint16_t* out = p.out + t * p.out_st + ((int64_t)g * p.group + team * GH) * D + e_tid;
+          const int64_t hq = t * p.Hq + (int64_t)g * p.group;
+          if (p.gate && at < p.group) mul *= 1.f / (1.f + expf(-p.gate[hq + at]));
+          uint16_t* out = p.out + t * p.out_st + (int64_t)g * p.group * D + tid;
 #pragma unroll
-          for (int h = 0; h < GH; ++h) {
+          for (int h = 0; h < HG; ++h) {
             const float m = __shfl_sync(0xffffffffu, mul, h);
-            if (h < heads) {
+            if (h < p.group) {
               out[h * D] = narrow<F16>((h & 1 ? o0[h / 2].y : o0[h / 2].x) * m);
               out[h * D + 128] = narrow<F16>((h & 1 ? o1[h / 2].y : o1[h / 2].x) * m);
             }
           }
-          if ((warp & 3) == 0 && lane < heads) {
+          if (warp == 0 && lane < p.group) {
             const float l2 = l == 0.f ? -INFINITY : mref_lane + log2f(l);
             if (p.lse) p.lse[hq + lane] = l2 * 0.69314718055994531f;
             if (p.lse2) p.lse2[hq + lane] = l2;
           }
         } else {
           // slot 2 i: the pair that run i begins with; 2 i + 1: the one it ends with
-          const int64_t head0 = (2 * (int64_t)blockIdx.x + (pair == pair0 ? 0 : 1)) * p.group + team * GH;
-          float* po = p.part_o + head0 * D + e_tid;
+          const int64_t slot = 2 * (int64_t)blockIdx.x + (pair == pair0 ? 0 : 1);
+          float* po = p.part_o + slot * p.group * D + tid;
 #pragma unroll
-          for (int h = 0; h < GH; ++h)
-            if (h < heads) {
+          for (int h = 0; h < HG; ++h)
+            if (h < p.group) {
               po[h * D] = h & 1 ? o0[h / 2].y : o0[h / 2].x;
               po[h * D + 128] = h & 1 ? o1[h / 2].y : o1[h / 2].x;
             }
-          if ((warp & 3) == 0 && lane < heads) {
-            p.part_ml[(head0 + lane) * 2] = l == 0.f ? -INFINITY : mref_lane;
-            p.part_ml[(head0 + lane) * 2 + 1] = l;
+          if (warp == 0 && lane < p.group) {
+            p.part_ml[(slot * p.group + lane) * 2] = l == 0.f ? -INFINITY : mref_lane;
+            p.part_ml[(slot * p.group + lane) * 2 + 1] = l;
           }
         }
       }
@@ -869,7 +887,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_fp8_kernel(const Params p) {
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, C::TMEM);
+  if (warp == 8) tmem_dealloc(tmem, C::TMEM);
 }
 
 // Merges the pieces of pairs cut by the end of a run: one warp per (cut, head).

@@ -146,18 +146,31 @@ qsa_status_t device_info(int* sms) {
         {reinterpret_cast<const void*>(qsa::prefill::prefill_kernel<false>), qsa::prefill::SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::prefill::prefill_kernel<true>), qsa::prefill::SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::attn::attn_kernel), qsa::attn::SMEM_BYTES},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 4>), qsa::attn8::Cfg<false>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 6>), qsa::attn8::Cfg<false>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>), qsa::attn8::Cfg<false>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 4>), qsa::attn8::Cfg<true>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 6>), qsa::attn8::Cfg<true>::SMEM},
-        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>), qsa::attn8::Cfg<true>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>), qsa::attn8::Cfg<false, 8>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 12>), qsa::attn8::Cfg<false, 12>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 16>), qsa::attn8::Cfg<false, 16>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>), qsa::attn8::Cfg<true, 8>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>), qsa::attn8::Cfg<true, 12>::SMEM},
+        {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 16>), qsa::attn8::Cfg<true, 16>::SMEM},
         {reinterpret_cast<const void*>(qsa::topk::topk_rows_kernel), qsa::topk::ROWS_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_pipe_kernel), qsa::topk::PIPE_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_filter_kernel), qsa::topk::TP_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_list_kernel),
          qsa::topk::TP_LIST_WARPS * qsa::topk::tp_list_warp_bytes(qsa::topk::MAX_W)},
     };
+    // These kernels share their launch registers out by setmaxnreg: fewer than they count on would never do.
+    for (const void* fn : {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 12>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 16>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>)}) {
+      cudaFuncAttributes a = {};
+      e = cudaFuncGetAttributes(&a, fn);
+      if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+      if (a.numRegs < qsa::attn8::REGS_LAUNCH)
+        return fail(QSA_ERR_UNSUPPORTED, "attention over the 8-bit cache was built with %d registers a thread; %d needed",
+                    a.numRegs, qsa::attn8::REGS_LAUNCH);
+    }
     for (auto& k : kernels) {
       e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.bytes);
       if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -434,9 +447,9 @@ void attn_splits(int64_t T, int32_t Hkv, int32_t width, int32_t* splits, int32_t
   *cps = (int32_t)per;
 }
 
-// Runs of the 8-bit cache's attention: one CTA on each of 148 SMs (a number of
+// Runs of the 8-bit cache's attention: two CTAs on each of 148 SMs (a number of
 // its own, so that the workspace depends on the shapes only), no more than tiles.
-constexpr int64_t kAttn8Runs = 148;
+constexpr int64_t kAttn8Runs = 296;
 
 int64_t attn8_tiles(int32_t width) { return std::max<int64_t>(1, ((int64_t)width + qsa::attn8::TILE - 1) / qsa::attn8::TILE); }
 
@@ -1249,9 +1262,9 @@ size_t qsa_sparse_attention_fp8_workspace_size(int64_t T, int32_t Hq, int32_t Hk
 }
 
 extern "C++" {
-template <bool F16, int GH>
+template <bool F16, int HG>
 static void launch_attn8(const qsa::attn8::Params& p, cudaStream_t s) {
-  qsa::attn8::attn_fp8_kernel<F16, GH><<<(unsigned)p.ctas, qsa::attn8::THREADS, qsa::attn8::Cfg<F16>::SMEM, s>>>(p);
+  qsa::attn8::attn_fp8_kernel<F16, HG><<<(unsigned)p.ctas, qsa::attn8::THREADS, qsa::attn8::Cfg<F16, HG>::SMEM, s>>>(p);
   const int64_t warps = (int64_t)(p.ctas - 1) * p.group;   // one per cut between runs and head
   if (warps > 0 && (p.total % p.ctas != 0 || (p.total / p.ctas) % p.tiles != 0))
     qsa::attn8::combine_fp8_kernel<F16><<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(p);
@@ -1364,7 +1377,8 @@ static qsa_status_t attention_fp8_common(
   p.total = T * Hkv * (int64_t)p.tiles;
   if (T * Hkv > INT32_MAX || p.total / kAttn8Runs * 2 >= INT32_MAX / 4)
     return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
-  p.ctas = (int32_t)std::min(p.total, kAttn8Runs);
+  const int HG = p.group <= 8 ? 8 : p.group <= 12 ? 12 : 16;   // query heads the kernel holds
+  p.ctas = (int32_t)std::min(p.total, f16 && HG == 16 ? kAttn8Runs / 2 : kAttn8Runs);
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
@@ -1377,15 +1391,14 @@ static qsa_status_t attention_fp8_common(
   p.weights = want_w ? weights : nullptr;
   p.w_stride = T > 1 ? weights_stride : width;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // query heads of a team: half of the group, in pairs
   if (f16) {
-    if (p.group <= 8) launch_attn8<true, 4>(p, s);
-    else if (p.group <= 12) launch_attn8<true, 6>(p, s);
-    else launch_attn8<true, 8>(p, s);
+    if (HG == 8) launch_attn8<true, 8>(p, s);
+    else if (HG == 12) launch_attn8<true, 12>(p, s);
+    else launch_attn8<true, 16>(p, s);
   } else {
-    if (p.group <= 8) launch_attn8<false, 4>(p, s);
-    else if (p.group <= 12) launch_attn8<false, 6>(p, s);
-    else launch_attn8<false, 8>(p, s);
+    if (HG == 8) launch_attn8<false, 8>(p, s);
+    else if (HG == 12) launch_attn8<false, 12>(p, s);
+    else launch_attn8<false, 16>(p, s);
   }
   if (want_w) weights_kernel<<<(unsigned)((T * width + 255) / 256), 256, 0, s>>>(p);
   return launch_status("8-bit cache attention kernels");
