@@ -439,74 +439,113 @@ def mqa_paged_batch(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Te
     return out
 
 
-def _placed(stream, *tensors):
-    """(device, stream handle) of a call on the given tensors (None skipped): they must all live on one device, and
-    the call runs there, on `stream` or on that device's current stream."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one call needs one device")
+# The calls on the 8-bit cache are short on the device, so their binding keeps the host's share small: plain integers
+# for pointers, every tensor's shape and strides read once, the checks in line.
+
+def _want(t, name, dtype, dim, dev):
+    """_need, and that the tensor lives on device ordinal `dev`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.dim() != dim:
+        _need(t, name, dtype, dim)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors on cuda:{dev}: one call needs one device")
+
+
+def _first(t, name):
+    """Device ordinal of a call's first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _raw_stream(stream, dev):
     if stream is None:
-        return dev, C.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-    return dev, _stream(stream)
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _new(stream, shape, dtype, dev):
     """Memory that belongs to the stream the call runs on (an output or a workspace made here)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+        stream = torch.cuda.ExternalStream(_raw_stream(stream, dev), device=_DEVICES[dev])
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
+
+
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
+_entries: dict = {}
 
 
 def _call(dev, name, *args):
-    """The library call with `dev` current."""
-    if dev.index == torch.cuda.current_device():
-        _check(name, getattr(lib(), name)(*args))
+    """The library call with device `dev` current."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(lib(), name)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args)
     else:
         with torch.cuda.device(dev):
-            _check(name, getattr(lib(), name)(*args))
+            status = fn(*args)
+    if status:
+        _check(name, status)
 
 
 def _workspace(workspace, need, stream, dev):
+    """(pointer, bytes, the tensor that owns it)"""
     if workspace is None:
-        workspace = _new(stream, (max(need, 16),), torch.uint8, dev)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
+        if need <= 0:
+            return 0, 0, None
+        workspace = _new(stream, (need,), torch.uint8, dev)
+        return workspace.data_ptr(), need, workspace
+    if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace, workspace.numel() * workspace.element_size()
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace is on cuda:{workspace.get_device()}, other tensors on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _cache8(k_cache, v_cache, k_scale, v_scale):
-    """Check the 8-bit cache's tensors; returns (codes of K, codes of V, block_tokens)."""
-    k_cache, v_cache = (c.view(torch.uint8) if isinstance(c, torch.Tensor) and c.dtype == torch.float8_e4m3fn else c
-                        for c in (k_cache, v_cache))
-    _need(k_cache, "k_cache", torch.uint8, 4)
-    _need(v_cache, "v_cache", torch.uint8, 4)
-    _need(k_scale, "k_scale", torch.float32, 3)
-    _need(v_scale, "v_scale", torch.float32, 3)
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.shape[3] != 256 \
-            or k_cache.stride(3) != 1:
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _cache8(k_cache, v_cache, k_scale, v_scale, dev):
+    """Check the 8-bit cache's tensors; returns (pages, page_size, Hkv, its C arguments from k_cache to Hkv)."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _CODES:
+            _need(t, n, torch.uint8, 4)
+        _want(t, n, t.dtype, 4, dev)
+    _want(k_scale, "k_scale", torch.float32, 3, dev)
+    _want(v_scale, "v_scale", torch.float32, 3, dev)
+    shape, strides = k_cache.shape, k_cache.stride()
+    pages, ps, Hkv, D = shape
+    if v_cache.shape != shape or v_cache.stride() != strides or D != 256 or strides[3] != 1:
         raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, 256] with the same strides")
-    pages, ps, Hkv, _ = k_cache.shape
-    blocks = k_scale.shape[1]
-    if k_scale.shape != v_scale.shape or k_scale.stride() != v_scale.stride() or k_scale.stride(2) != 1 \
-            or k_scale.shape[0] != pages or k_scale.shape[2] != Hkv or blocks < 1 or ps % blocks:
+    sc_shape, sc_strides = k_scale.shape, k_scale.stride()
+    blocks = sc_shape[1]
+    if v_scale.shape != sc_shape or v_scale.stride() != sc_strides or sc_strides[2] != 1 or sc_shape[0] != pages \
+            or sc_shape[2] != Hkv or blocks < 1 or ps % blocks:
         raise ValueError("k_scale and v_scale must be [pages, blocks, Hkv] with the same strides, unit head stride, "
                          "and blocks must divide page_size")
-    return k_cache, v_cache, ps // blocks
+    return pages, ps, Hkv, (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, ps,
+                            ps // blocks, strides[0], strides[1], strides[2], sc_strides[0], sc_strides[1], Hkv)
 
 
-def _tables(page_table, cu_seqlens_q, seq_lens):
-    _need(page_table, "page_table", torch.int32, 2)
-    _index_checks(cu_seqlens_q, seq_lens)
-    if page_table.stride(1) != 1 or page_table.shape[0] != seq_lens.shape[0]:
+def _tables(page_table, cu_seqlens_q, seq_lens, dev):
+    """Check the batch's tables; returns their C arguments from page_table to R."""
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
+    _want(seq_lens, "seq_lens", torch.int32, 1, dev)
+    R, max_pages = page_table.shape
+    pt_strides = page_table.stride()
+    if seq_lens.shape[0] != R or pt_strides[1] != 1:
         raise ValueError("page_table needs one row per request and a unit column stride")
+    if cu_seqlens_q.shape[0] != R + 1 or not cu_seqlens_q.is_contiguous() or not seq_lens.is_contiguous():
+        raise ValueError("cu_seqlens_q must have one more entry than seq_lens, both contiguous")
+    return page_table.data_ptr(), pt_strides[0], max_pages, cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), R
 
 
-def _token_weight(token_weight, pages, page_size):
-    _need(token_weight, "token_weight", torch.int64, 2)
+def _token_weight(token_weight, pages, page_size, dev):
+    _want(token_weight, "token_weight", torch.int64, 2, dev)
     if token_weight.shape != (pages, page_size) or not token_weight.is_contiguous():
         raise ValueError("token_weight must be contiguous int64 [pages, page_size]")
 
@@ -519,23 +558,21 @@ def kv_append_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
     block_tokens, Hkv].  Row i of request r goes to position seq_lens[r] - qlen_r + i.  A block's scale is the
     smallest power of two that holds it; it grows when a later token needs it.  token_weight (int64 [pages,
     page_size]) is zeroed for the tokens written."""
-    dt = k.dtype if isinstance(k, torch.Tensor) and k.dtype == torch.float16 else torch.bfloat16
-    _need(k, "k", dt, 3)
-    _need(v, "v", dt, 3)
-    k_cache, v_cache, bt = _cache8(k_cache, v_cache, k_scale, v_scale)
-    _tables(page_table, cu_seqlens_q, seq_lens)
-    pages, ps, Hkv, _ = k_cache.shape
-    if k.shape != v.shape or k.shape[1:] != (Hkv, 256) or k.stride(2) != 1 or v.stride(2) != 1:
+    dev = _first(k, "k")
+    dt = torch.float16 if k.dtype == torch.float16 else torch.bfloat16
+    _want(k, "k", dt, 3, dev)
+    _want(v, "v", dt, 3, dev)
+    pages, ps, Hkv, cache = _cache8(k_cache, v_cache, k_scale, v_scale, dev)
+    tables = _tables(page_table, cu_seqlens_q, seq_lens, dev)
+    shape, ks, vs = k.shape, k.stride(), v.stride()
+    T = shape[0]
+    if v.shape != shape or shape[1] != Hkv or shape[2] != 256 or ks[2] != 1 or vs[2] != 1:
         raise ValueError("k and v must be [T, Hkv, 256] with unit feature stride")
     if token_weight is not None:
-        _token_weight(token_weight, pages, ps)
-    dev, st = _placed(stream, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seq_lens,
-                      token_weight)
-    _call(dev, "qsa_kv_append_fp8_f16" if dt == torch.float16 else "qsa_kv_append_fp8",
-          _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _ptr(k_cache), _ptr(v_cache),
-          _ptr(k_scale), _ptr(v_scale), pages, ps, bt, k_cache.stride(0), k_cache.stride(1), k_cache.stride(2),
-          k_scale.stride(0), k_scale.stride(1), Hkv, _ptr(page_table), page_table.stride(0), page_table.shape[1],
-          _ptr(cu_seqlens_q), _ptr(seq_lens), seq_lens.shape[0], k.shape[0], _ptr(token_weight), st)
+        _token_weight(token_weight, pages, ps, dev)
+    _call(dev, "qsa_kv_append_fp8_f16" if dt == torch.float16 else "qsa_kv_append_fp8", k.data_ptr(), ks[0], ks[1],
+          v.data_ptr(), vs[0], vs[1], *cache, *tables, T, None if token_weight is None else token_weight.data_ptr(),
+          _raw_stream(stream, dev))
 
 
 def sparse_attention_fp8_workspace_size(T: int, Hq: int, Hkv: int, width: int, weights: bool = False) -> int:
@@ -552,47 +589,54 @@ def sparse_attention_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     [T, Hq, 256], lse fp32 [T, Hq]).  weights (fp32 [T, width]), if given, receives every entry's softmax
     probability summed over the query heads.  The workspace (any CUDA tensor, 16-byte aligned) is allocated here by
     torch when not given."""
-    dt = q.dtype if isinstance(q, torch.Tensor) and q.dtype == torch.float16 else torch.bfloat16
-    _need(q, "q", dt, 3)
-    k_cache, v_cache, bt = _cache8(k_cache, v_cache, k_scale, v_scale)
-    _tables(page_table, cu_seqlens_q, seq_lens)
-    _need(token_idx, "token_idx", torch.int32, 2)
+    dev = _first(q, "q")
+    dt = torch.float16 if q.dtype == torch.float16 else torch.bfloat16
+    _want(q, "q", dt, 3, dev)
+    pages, ps, Hkv, cache = _cache8(k_cache, v_cache, k_scale, v_scale, dev)
+    tables = _tables(page_table, cu_seqlens_q, seq_lens, dev)
+    _want(token_idx, "token_idx", torch.int32, 2, dev)
     T, Hq, Dq = q.shape
-    pages, ps, Hkv, _ = k_cache.shape
-    width = token_idx.shape[1]
-    if Dq != 256 or q.stride(2) != 1:
+    qs, ts = q.stride(), token_idx.stride()
+    rows, width = token_idx.shape
+    if Dq != 256 or qs[2] != 1:
         raise ValueError("q must be [T, Hq, 256] with unit feature stride")
-    if token_idx.shape[0] != T or token_idx.stride(1) != 1:
+    if rows != T or ts[1] != 1:
         raise ValueError("token_idx must be [T, width] with unit column stride")
+    gate_p = weights_p = None
+    ws0 = 0
     if gate is not None:
-        _need(gate, "gate", torch.float32, 2)
+        _want(gate, "gate", torch.float32, 2, dev)
         if gate.shape != (T, Hq) or not gate.is_contiguous():
             raise ValueError("gate must be contiguous fp32 [T, Hq]")
+        gate_p = gate.data_ptr()
     if weights is not None:
-        _need(weights, "weights", torch.float32, 2)
-        if weights.shape != (T, width) or weights.stride(1) != 1:
+        _want(weights, "weights", torch.float32, 2, dev)
+        ws0, ws1 = weights.stride()
+        if weights.shape != (T, width) or ws1 != 1:
             raise ValueError("weights must be fp32 [T, width] with unit column stride")
-    dev, st = _placed(stream, q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seq_lens, token_idx,
-                      gate, out, lse, weights, workspace)
+        weights_p = weights.data_ptr()
     if out is None:
         out = _new(stream, (T, Hq, 256), dt, dev)
-    _need(out, "out", dt, 3)
-    if out.shape != (T, Hq, 256) or out.stride(2) != 1 or out.stride(1) != 256:
-        raise ValueError("out must be [T, Hq, 256] with contiguous heads")
+        out0 = Hq * 256
+    else:
+        _want(out, "out", dt, 3, dev)
+        out0, out1, out2 = out.stride()
+        if out.shape != (T, Hq, 256) or out2 != 1 or out1 != 256:
+            raise ValueError("out must be [T, Hq, 256] with contiguous heads")
     if lse is None:
         lse = _new(stream, (T, Hq), torch.float32, dev)
-    _need(lse, "lse", torch.float32, 2)
-    if lse.shape != (T, Hq) or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous fp32 [T, Hq]")
-    workspace, nbytes = _workspace(
-        workspace, sparse_attention_fp8_workspace_size(T, Hq, Hkv, max(width, 1), weights is not None), stream, dev)
+    else:
+        _want(lse, "lse", torch.float32, 2, dev)
+        if lse.shape != (T, Hq) or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous fp32 [T, Hq]")
+    need = 0
+    if workspace is None:
+        need = lib().qsa_sparse_attention_fp8_workspace_size(T, Hq, Hkv, width if width > 0 else 1,
+                                                             0 if weights is None else 1)
+    wp, nbytes, workspace = _workspace(workspace, need, stream, dev)
     _call(dev, "qsa_sparse_attention_fp8_f16" if dt == torch.float16 else "qsa_sparse_attention_fp8",
-          _ptr(q), q.stride(0), q.stride(1), Hq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages, ps,
-          bt, k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), k_scale.stride(0), k_scale.stride(1), Hkv,
-          _ptr(page_table), page_table.stride(0), page_table.shape[1], _ptr(cu_seqlens_q), _ptr(seq_lens),
-          seq_lens.shape[0], _ptr(token_idx), token_idx.stride(0), width, T, _ptr(gate), float(scale), _ptr(out),
-          out.stride(0), _ptr(lse), _ptr(weights), weights.stride(0) if weights is not None else 0, _ptr(workspace),
-          nbytes, st)
+          q.data_ptr(), qs[0], qs[1], Hq, *cache, *tables, token_idx.data_ptr(), ts[0], width, T, gate_p, scale,
+          out.data_ptr(), out0, lse.data_ptr(), weights_p, ws0, wp, nbytes, _raw_stream(stream, dev))
     return out, lse
 
 
@@ -601,19 +645,20 @@ def accumulate_weights(weights: torch.Tensor, token_idx: torch.Tensor, page_tabl
                        stream=None) -> torch.Tensor:
     """Add attention weights (fp32 [T, width], one per entry of token_idx int32 [T, width]) up per cached token, in
     place: token_weight int64 [pages, page_size] in units of 2^-32.  Returns token_weight."""
-    _need(weights, "weights", torch.float32, 2)
-    _need(token_idx, "token_idx", torch.int32, 2)
-    _need(token_weight, "token_weight", torch.int64, 2)
-    _tables(page_table, cu_seqlens_q, seq_lens)
+    dev = _first(weights, "weights")
+    _want(weights, "weights", torch.float32, 2, dev)
+    _want(token_idx, "token_idx", torch.int32, 2, dev)
+    _want(token_weight, "token_weight", torch.int64, 2, dev)
+    tables = _tables(page_table, cu_seqlens_q, seq_lens, dev)
     pages, ps = token_weight.shape
-    _token_weight(token_weight, pages, ps)
-    T, width = token_idx.shape
-    if weights.shape != (T, width) or weights.stride(1) != 1 or token_idx.stride(1) != 1:
+    T, width = shape = token_idx.shape
+    ws, ts = weights.stride(), token_idx.stride()
+    if not token_weight.is_contiguous():
+        raise ValueError("token_weight must be contiguous int64 [pages, page_size]")
+    if weights.shape != shape or ws[1] != 1 or ts[1] != 1:
         raise ValueError("weights and token_idx must be [T, width] with unit column strides")
-    dev, st = _placed(stream, weights, token_idx, page_table, cu_seqlens_q, seq_lens, token_weight)
-    _call(dev, "qsa_accumulate_weights", _ptr(weights), weights.stride(0), _ptr(token_idx), token_idx.stride(0), width,
-          T, _ptr(page_table), page_table.stride(0), page_table.shape[1], _ptr(cu_seqlens_q), _ptr(seq_lens),
-          seq_lens.shape[0], _ptr(token_weight), pages, ps, st)
+    _call(dev, "qsa_accumulate_weights", weights.data_ptr(), ws[0], token_idx.data_ptr(), ts[0], width, T, *tables,
+          token_weight.data_ptr(), pages, ps, _raw_stream(stream, dev))
     return token_weight
 
 
@@ -629,30 +674,43 @@ def evict_pages(token_weight: torch.Tensor, page_table: torch.Tensor, seq_lens: 
     keep[r] (int32 [R]) live pages; its first keep_first and last keep_last logical pages stay.  Returns (table_out
     int32 [R, max_pages] with -1 for dropped pages, freed int32 [R, max_pages]: the dropped pages in order, then -1,
     counts int32 [R]).  table_out may be page_table."""
-    _need(token_weight, "token_weight", torch.int64, 2)
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(keep, "keep", torch.int32, 1)
+    dev = _first(token_weight, "token_weight")
+    _want(token_weight, "token_weight", torch.int64, 2, dev)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    _want(seq_lens, "seq_lens", torch.int32, 1, dev)
+    _want(keep, "keep", torch.int32, 1, dev)
     pages, ps = token_weight.shape
-    _token_weight(token_weight, pages, ps)
-    R, max_pages = page_table.shape
+    R, max_pages = shape = page_table.shape
+    pts = page_table.stride()
+    if not token_weight.is_contiguous():
+        raise ValueError("token_weight must be contiguous int64 [pages, page_size]")
     if seq_lens.shape[0] != R or keep.shape[0] != R or not seq_lens.is_contiguous() or not keep.is_contiguous() \
-            or page_table.stride(1) != 1:
+            or pts[1] != 1:
         raise ValueError("page_table needs one row per request and a unit column stride, seq_lens and keep one "
                          "contiguous entry per request")
-    dev, st = _placed(stream, token_weight, page_table, seq_lens, keep, table_out, freed, counts, workspace)
-    table_out = _new(stream, (R, max_pages), torch.int32, dev) if table_out is None else table_out
-    freed = _new(stream, (R, max_pages), torch.int32, dev) if freed is None else freed
-    counts = _new(stream, (R,), torch.int32, dev) if counts is None else counts
+    strides = []
+    made = []
     for t, n in ((table_out, "table_out"), (freed, "freed")):
-        _need(t, n, torch.int32, 2)
-        if t.shape != (R, max_pages) or t.stride(1) != 1:
+        if t is None:
+            made.append(_new(stream, (R, max_pages), torch.int32, dev))
+            strides.append(max_pages)
+            continue
+        _want(t, n, torch.int32, 2, dev)
+        s0, s1 = t.stride()
+        if t.shape != shape or s1 != 1:
             raise ValueError(f"{n} must be int32 [R, max_pages] with unit column stride")
-    _need(counts, "counts", torch.int32, 1)
-    if counts.shape[0] != R or not counts.is_contiguous():
-        raise ValueError("counts must be contiguous int32 [R]")
-    workspace, nbytes = _workspace(workspace, evict_pages_workspace_size(R, max_pages), stream, dev)
-    _call(dev, "qsa_evict_pages", _ptr(token_weight), pages, ps, _ptr(page_table), page_table.stride(0), max_pages,
-          _ptr(seq_lens), _ptr(keep), R, int(keep_first), int(keep_last), _ptr(table_out), table_out.stride(0),
-          _ptr(freed), freed.stride(0), _ptr(counts), _ptr(workspace), nbytes, st)
+        made.append(t)
+        strides.append(s0)
+    table_out, freed = made
+    if counts is None:
+        counts = _new(stream, (R,), torch.int32, dev)
+    else:
+        _want(counts, "counts", torch.int32, 1, dev)
+        if counts.shape[0] != R or not counts.is_contiguous():
+            raise ValueError("counts must be contiguous int32 [R]")
+    wp, nbytes, workspace = _workspace(workspace, evict_pages_workspace_size(R, max_pages) if workspace is None else 0,
+                                       stream, dev)
+    _call(dev, "qsa_evict_pages", token_weight.data_ptr(), pages, ps, page_table.data_ptr(), pts[0], max_pages,
+          seq_lens.data_ptr(), keep.data_ptr(), R, keep_first, keep_last, table_out.data_ptr(), strides[0],
+          freed.data_ptr(), strides[1], counts.data_ptr(), wp, nbytes, _raw_stream(stream, dev))
     return table_out, freed, counts

@@ -132,8 +132,8 @@ struct Params {
   int32_t width;
   int64_t T;
   int32_t tiles;              // tiles of one (row, KV head) pair
-  int64_t total;              // tiles of all pairs
-  int32_t ctas;               // runs
+  int32_t ctas;               // runs: each has `per` tiles, the first `more` of them one more
+  int32_t per, more;
   float scale_log2;
   float* part_o;              // [2 ctas, group, 256] unnormalised outputs of pairs cut by a run's ends
   float* part_ml;             // [2 ctas, group, 2] maximum (log2 units), sum
@@ -147,16 +147,8 @@ struct Params {
   int64_t w_stride;
 };
 
-// First tile of run i: the runs differ by at most one tile.
-__device__ __forceinline__ int64_t run_begin(const Params& p, int64_t i) {
-  const int64_t per = p.total / p.ctas, more = p.total % p.ctas;
-  return i * per + (i < more ? i : more);
-}
-// The run that holds tile u.
-__device__ __forceinline__ int64_t run_of(const Params& p, int64_t u) {
-  const int64_t per = p.total / p.ctas, more = p.total % p.ctas;
-  return u < more * (per + 1) ? u / (per + 1) : more + (u - more * (per + 1)) / per;
-}
+// First tile of run i.
+__device__ __forceinline__ int run_begin(const Params& p, int i) { return i * p.per + min(i, p.more); }
 
 // Shared-memory descriptor of an unswizzled N-major operand: cores of 8 K
 // rows of 16 bytes, k8_stride bytes from one to the next along K and
@@ -412,10 +404,8 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
   volatile int* add_s = abort + 1;                     // whether the next output product adds to what TMEM holds
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t u0 = run_begin(p, blockIdx.x);
-  const int n = (int)(run_begin(p, (int64_t)blockIdx.x + 1) - u0);
-  const int pair0 = (int)(u0 / p.tiles);
-  const int tile0 = (int)(u0 - (int64_t)pair0 * p.tiles);
+  const int u0 = run_begin(p, blockIdx.x), n = run_begin(p, blockIdx.x + 1) - u0;
+  const int pair0 = u0 / p.tiles, tile0 = u0 - pair0 * p.tiles;
 
   if (warp == 8) tmem_alloc(tmem_s, C::TMEM);
   if (tid == 0) {
@@ -887,49 +877,67 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
   }
   tc_fence_before();
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 8) tmem_dealloc(tmem, C::TMEM);
 }
 
-// Merges the pieces of pairs cut by the end of a run: one warp per (cut, head).
-// The warps of a pair's first cut merge all of its pieces.
+// Merges the pieces of pairs cut by the end of a run: one CTA per (cut, 4
+// heads), two features a thread.  The CTAs of a pair's first cut merge all of its
+// pieces.  It is launched while the attention runs and waits for it.
+constexpr int MERGE_HEADS = 4, MERGE_THREADS = MERGE_HEADS * D / 2;
+
 template <bool F16>
-__global__ void __launch_bounds__(256) combine_fp8_kernel(const Params p) {
-  const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int64_t cut = wid / p.group + 1;               // between runs cut - 1 and cut
-  const int hh = (int)(wid % p.group);
-  if (cut >= p.ctas) return;
-  const int64_t at = run_begin(p, cut), pair = at / p.tiles, begin = pair * p.tiles;
-  if (at == begin) return;                             // the runs part between two pairs
-  const int64_t first = run_of(p, begin), last = run_of(p, begin + p.tiles - 1);
-  if (cut != first + 1) return;
-  float M = -INFINITY;
-  for (int64_t i = first; i <= last; ++i) {
-    const int64_t slot = 2 * i + (run_begin(p, i) >= begin || i > first ? 0 : 1);
-    M = fmaxf(M, p.part_ml[(slot * p.group + hh) * 2]);
-  }
-  const float Mr = M == -INFINITY ? 0.f : M;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
-  for (int64_t i = first; i <= last; ++i) {
-    const int64_t slot = 2 * i + (run_begin(p, i) >= begin || i > first ? 0 : 1);
-    const float w = exp2f(p.part_ml[(slot * p.group + hh) * 2] - Mr);
-    sum = fmaf(w, p.part_ml[(slot * p.group + hh) * 2 + 1], sum);
-    const float* po = p.part_o + (slot * p.group + hh) * D + lane * 8;
+__global__ void __launch_bounds__(MERGE_THREADS) combine_fp8_kernel(const Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int cut = blockIdx.x + 1;                      // between runs cut - 1 and cut
+  const int hh = blockIdx.y * MERGE_HEADS + threadIdx.x / (D / 2), f2 = threadIdx.x % (D / 2);
+  const int at = run_begin(p, cut), pair = at / p.tiles, begin = pair * p.tiles, first = cut - 1;
+  // no cut inside a pair, or not the pair's first one
+  if (at == begin || (first > 0 && run_begin(p, first) > begin) || hh >= p.group) return;
+  int pieces = 2;
+  while (first + pieces < p.ctas && run_begin(p, first + pieces) < begin + p.tiles) ++pieces;
+  // the first piece ends run `first` (its second slot unless the run begins with this pair); the others begin theirs
+  const int slot0 = 2 * first + (run_begin(p, first) >= begin ? 0 : 1);
+  auto slot = [&](int i) { return (int64_t)(i == 0 ? slot0 : 2 * (first + i)) * p.group + hh; };
+  // (plain loads: the pieces are written while this grid is already launched)
+  float M = -INFINITY, sum = 0.f;
+  float2 acc = make_float2(0.f, 0.f);
+  constexpr int BATCH = 8;                             // pieces loaded in one round trip
+  for (int i0 = 0; i0 < pieces; i0 += BATCH) {
+    float2 ml[BATCH], o[BATCH];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, po[e], acc[e]);
+    for (int i = 0; i < BATCH; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      o[i] = make_float2(0.f, 0.f);
+      if (i0 + i < pieces) {
+        ml[i] = *reinterpret_cast<const float2*>(p.part_ml + slot(i0 + i) * 2);
+        o[i] = reinterpret_cast<const float2*>(p.part_o + slot(i0 + i) * D)[f2];
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) m = fmaxf(m, ml[i].x);
+    const float mr = m == -INFINITY ? 0.f : m;
+    const float a = exp2f(M - mr);                     // 0 while nothing was visible
+    M = m;
+    sum *= a;
+    acc = make_float2(acc.x * a, acc.y * a);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const float w = exp2f(ml[i].x - mr);
+      sum = fmaf(w, ml[i].y, sum);
+      acc.x = fmaf(w, o[i].x, acc.x);
+      acc.y = fmaf(w, o[i].y, acc.y);
+    }
   }
   const int64_t t = pair / p.Hkv;
-  const int h = (int)(pair - t * p.Hkv) * p.group + hh;
+  const int h = (pair - (int)t * p.Hkv) * p.group + hh;
   float mul = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // a NaN sum stays NaN
   if (p.gate) mul *= 1.f / (1.f + expf(-p.gate[t * p.Hq + h]));
-  uint32_t w4[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    w4[e] = (uint32_t)narrow<F16>(acc[2 * e] * mul) | ((uint32_t)narrow<F16>(acc[2 * e + 1] * mul) << 16);
-  *reinterpret_cast<uint4*>(p.out + t * p.out_st + (int64_t)h * D + lane * 8) =
-      make_uint4(w4[0], w4[1], w4[2], w4[3]);
-  if (lane == 0) {
+  reinterpret_cast<uint32_t*>(p.out + t * p.out_st + (int64_t)h * D)[f2] =
+      (uint32_t)narrow<F16>(acc.x * mul) | ((uint32_t)narrow<F16>(acc.y * mul) << 16);
+  if (f2 == 0) {
     const float l2 = sum == 0.f ? -INFINITY : M + log2f(sum);
     if (p.lse) p.lse[t * p.Hq + h] = l2 * 0.69314718055994531f;
     if (p.lse2) p.lse2[t * p.Hq + h] = l2;
@@ -939,16 +947,18 @@ __global__ void __launch_bounds__(256) combine_fp8_kernel(const Params p) {
 // weights[t, e] = sum over query heads of 2^(s - lse2): one thread per entry,
 // heads in order.
 __global__ void __launch_bounds__(256) weights_kernel(const Params p) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= p.T * p.width) return;
-  const int64_t t = i / p.width;
-  const int e = (int)(i % p.width);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t t = blockIdx.y;
+  const int e = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+  if (e >= p.width) return;
   float w = 0.f;
   for (int g = 0; g < p.Hkv; ++g) {
     const float* s = p.part_s + ((t * p.Hkv + g) * p.width + e) * p.group;
+    const float* l = p.lse2 + t * p.Hq + g * p.group;
+#pragma unroll 4
     for (int h = 0; h < p.group; ++h) {
       const float x = s[h];
-      if (x != -INFINITY) w += exp2f(x - p.lse2[t * p.Hq + g * p.group + h]);
+      w += x == -INFINITY ? 0.f : exp2f(x - l[h]);
     }
   }
   p.weights[t * p.w_stride + e] = w;

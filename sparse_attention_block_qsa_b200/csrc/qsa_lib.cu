@@ -1265,9 +1265,10 @@ extern "C++" {
 template <bool F16, int HG>
 static void launch_attn8(const qsa::attn8::Params& p, cudaStream_t s) {
   qsa::attn8::attn_fp8_kernel<F16, HG><<<(unsigned)p.ctas, qsa::attn8::THREADS, qsa::attn8::Cfg<F16, HG>::SMEM, s>>>(p);
-  const int64_t warps = (int64_t)(p.ctas - 1) * p.group;   // one per cut between runs and head
-  if (warps > 0 && (p.total % p.ctas != 0 || (p.total / p.ctas) % p.tiles != 0))
-    qsa::attn8::combine_fp8_kernel<F16><<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(p);
+  if (p.ctas > 1 && (p.more != 0 || p.per % p.tiles != 0))   // some run ends inside a pair
+    launch_pdl(qsa::attn8::combine_fp8_kernel<F16>,
+               dim3((unsigned)p.ctas - 1, (unsigned)((p.group + qsa::attn8::MERGE_HEADS - 1) / qsa::attn8::MERGE_HEADS)),
+               dim3(qsa::attn8::MERGE_THREADS), 0, s, p);
 }
 }  // extern "C++"
 
@@ -1337,7 +1338,6 @@ static qsa_status_t attention_fp8_common(
   if (rows >= INT32_MAX)
     return fail(QSA_ERR_UNSUPPORTED, "the cache spans %lld rows of %lld bytes (the strides' greatest common divisor); "
                 "2^31 - 2 supported", (long long)rows, (long long)pitch);
-  if (want_w && T * width > (int64_t)INT32_MAX * 256) return fail(QSA_ERR_UNSUPPORTED, "too many entries for one launch");
   int sms = 0;
   st = device_info(&sms);
   if (st != QSA_OK) return st;
@@ -1374,11 +1374,12 @@ static qsa_status_t attention_fp8_common(
   p.width = width;
   p.T = T;
   p.tiles = (int32_t)attn8_tiles(width1);
-  p.total = T * Hkv * (int64_t)p.tiles;
-  if (T * Hkv > INT32_MAX || p.total / kAttn8Runs * 2 >= INT32_MAX / 4)
-    return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
+  const int64_t total = T * Hkv * (int64_t)p.tiles;
+  if (total > INT32_MAX / 2) return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
   const int HG = p.group <= 8 ? 8 : p.group <= 12 ? 12 : 16;   // query heads the kernel holds
-  p.ctas = (int32_t)std::min(p.total, f16 && HG == 16 ? kAttn8Runs / 2 : kAttn8Runs);
+  p.ctas = (int32_t)std::min(total, f16 && HG == 16 ? kAttn8Runs / 2 : kAttn8Runs);
+  p.per = (int32_t)(total / p.ctas);
+  p.more = (int32_t)(total % p.ctas);
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
@@ -1400,7 +1401,15 @@ static qsa_status_t attention_fp8_common(
     else if (HG == 12) launch_attn8<false, 12>(p, s);
     else launch_attn8<false, 16>(p, s);
   }
-  if (want_w) weights_kernel<<<(unsigned)((T * width + 255) / 256), 256, 0, s>>>(p);
+  // rows in grid y, at most 65,535 a launch
+  for (int64_t r0 = 0; want_w && r0 < T; r0 += 65535) {
+    const int64_t rows_w = std::min<int64_t>(T - r0, 65535);
+    Params pw = p;
+    pw.part_s += r0 * Hkv * width * p.group;
+    pw.lse2 += r0 * Hq;
+    pw.weights += r0 * p.w_stride;
+    launch_pdl(weights_kernel, dim3((unsigned)((width + 255) / 256), (unsigned)rows_w), dim3(256), 0, s, pw);
+  }
   return launch_status("8-bit cache attention kernels");
 }
 
