@@ -442,6 +442,10 @@ def mqa_paged_batch(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Te
 # The calls on the 8-bit cache are short on the device, so their binding keeps the host's share small: plain integers
 # for pointers, every tensor's shape and strides read once, the checks in line.
 
+def _fits(t, dtype, dim, dev):
+    return t.dtype is dtype and t.get_device() == dev and t.dim() == dim
+
+
 def _want(t, name, dtype, dim, dev):
     """_need, and that the tensor lives on device ordinal `dev`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.dim() != dim:
@@ -506,16 +510,24 @@ def _workspace(workspace, need, stream, dev):
 
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _cache8(k_cache, v_cache, k_scale, v_scale, dev):
     """Check the 8-bit cache's tensors; returns (pages, page_size, Hkv, its C arguments from k_cache to Hkv)."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or t.dtype not in _CODES:
-            _need(t, n, torch.uint8, 4)
-        _want(t, n, t.dtype, 4, dev)
-    _want(k_scale, "k_scale", torch.float32, 3, dev)
-    _want(v_scale, "v_scale", torch.float32, 3, dev)
+    try:
+        dt = k_cache.dtype
+        ok = dt in _CODES and v_cache.dtype in _CODES and _fits(k_cache, dt, 4, dev) \
+            and _fits(v_cache, v_cache.dtype, 4, dev) and _fits(k_scale, _F32, 3, dev) and _fits(v_scale, _F32, 3, dev)
+    except AttributeError:
+        ok = False
+    if not ok:
+        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            if not isinstance(t, torch.Tensor) or t.dtype not in _CODES:
+                _need(t, n, torch.uint8, 4)
+            _want(t, n, t.dtype, 4, dev)
+        _want(k_scale, "k_scale", torch.float32, 3, dev)
+        _want(v_scale, "v_scale", torch.float32, 3, dev)
     shape, strides = k_cache.shape, k_cache.stride()
     pages, ps, Hkv, D = shape
     if v_cache.shape != shape or v_cache.stride() != strides or D != 256 or strides[3] != 1:
@@ -532,9 +544,14 @@ def _cache8(k_cache, v_cache, k_scale, v_scale, dev):
 
 def _tables(page_table, cu_seqlens_q, seq_lens, dev):
     """Check the batch's tables; returns their C arguments from page_table to R."""
-    _want(page_table, "page_table", torch.int32, 2, dev)
-    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
-    _want(seq_lens, "seq_lens", torch.int32, 1, dev)
+    try:
+        ok = _fits(page_table, _I32, 2, dev) and _fits(cu_seqlens_q, _I32, 1, dev) and _fits(seq_lens, _I32, 1, dev)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _want(page_table, "page_table", torch.int32, 2, dev)
+        _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
+        _want(seq_lens, "seq_lens", torch.int32, 1, dev)
     R, max_pages = page_table.shape
     pt_strides = page_table.stride()
     if seq_lens.shape[0] != R or pt_strides[1] != 1:
@@ -688,20 +705,17 @@ def evict_pages(token_weight: torch.Tensor, page_table: torch.Tensor, seq_lens: 
             or pts[1] != 1:
         raise ValueError("page_table needs one row per request and a unit column stride, seq_lens and keep one "
                          "contiguous entry per request")
-    strides = []
-    made = []
-    for t, n in ((table_out, "table_out"), (freed, "freed")):
-        if t is None:
-            made.append(_new(stream, (R, max_pages), torch.int32, dev))
-            strides.append(max_pages)
-            continue
-        _want(t, n, torch.int32, 2, dev)
-        s0, s1 = t.stride()
-        if t.shape != shape or s1 != 1:
-            raise ValueError(f"{n} must be int32 [R, max_pages] with unit column stride")
-        made.append(t)
-        strides.append(s0)
-    table_out, freed = made
+    if table_out is None and freed is None:
+        table_out, freed = _new(stream, (2, R, max_pages), torch.int32, dev).unbind(0)
+        out0 = freed0 = max_pages
+    else:
+        table_out = _new(stream, (R, max_pages), torch.int32, dev) if table_out is None else table_out
+        freed = _new(stream, (R, max_pages), torch.int32, dev) if freed is None else freed
+        for t, n in ((table_out, "table_out"), (freed, "freed")):
+            _want(t, n, torch.int32, 2, dev)
+            if t.shape != shape or t.stride(1) != 1:
+                raise ValueError(f"{n} must be int32 [R, max_pages] with unit column stride")
+        out0, freed0 = table_out.stride(0), freed.stride(0)
     if counts is None:
         counts = _new(stream, (R,), torch.int32, dev)
     else:
@@ -711,6 +725,6 @@ def evict_pages(token_weight: torch.Tensor, page_table: torch.Tensor, seq_lens: 
     wp, nbytes, workspace = _workspace(workspace, evict_pages_workspace_size(R, max_pages) if workspace is None else 0,
                                        stream, dev)
     _call(dev, "qsa_evict_pages", token_weight.data_ptr(), pages, ps, page_table.data_ptr(), pts[0], max_pages,
-          seq_lens.data_ptr(), keep.data_ptr(), R, keep_first, keep_last, table_out.data_ptr(), strides[0],
-          freed.data_ptr(), strides[1], counts.data_ptr(), wp, nbytes, _raw_stream(stream, dev))
+          seq_lens.data_ptr(), keep.data_ptr(), R, keep_first, keep_last, table_out.data_ptr(), out0,
+          freed.data_ptr(), freed0, counts.data_ptr(), wp, nbytes, _raw_stream(stream, dev))
     return table_out, freed, counts

@@ -6,11 +6,11 @@
 //    (amax <= 448 s), so the codes lose nothing to the scale, a grown scale
 //    moves old codes by whole exponents (only what falls below E4M3's
 //    normal range is rounded again), and attention reads back exact products.
-//  * accumulate_kernel: one warp per 128 list entries of a row.  Weights are
+//  * accumulate_kernel: a warp per run of a row's list entries.  Weights are
 //    counted in units of 2^-32 in 64-bit integers: the order of the atomics
 //    cannot change the sums.
-//  * page_weight_kernel, evict_kernel: one warp per logical page sums its
-//    tokens; one CTA per request finds the lightest pages by a radix
+//  * page_weight_kernel, evict_kernel: groups of lanes sum the tokens of a
+//    logical page each; one CTA per request finds the lightest pages by a radix
 //    selection over the 64-bit sums and writes the new table and the freed
 //    pages in order.
 #pragma once
@@ -75,7 +75,11 @@ __device__ __forceinline__ uint2 encode8(const float* x) {
 }
 
 // Slots of scale blocks: request r owns slots cu[r] / bt + 2 r onwards, which
-// are enough (qlen rows touch at most qlen / bt + 2 blocks).
+// are enough (qlen rows touch at most qlen / bt + 2 blocks).  Up to HELD rows a
+// warp stay in registers between the maximum and the quantisation; the rows of
+// larger blocks are read again (out of L1 or L2).
+constexpr int HELD = 4;
+
 template <bool F16>
 __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendParams p) {
   __shared__ float top_s[APPEND_WARPS];
@@ -83,17 +87,20 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendP
   const int64_t slot = blockIdx.x;
   const int h = blockIdx.y, which = blockIdx.z;
   const int bt = p.block_tokens;
-  int lo = 0, hi = p.R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)(__ldg(p.cu + mid) / bt) + 2 * (int64_t)mid <= slot) lo = mid;
-    else hi = mid - 1;
+  // the last request whose slots begin at or before this one, 32 candidates a round trip
+  int r = 0, left = p.R;
+  while (left > 1) {
+    const int step = (left + 31) >> 5, i = r + lane * step;
+    const bool le = i < r + left && (int64_t)(__ldg(p.cu + i) / bt) + 2 * (int64_t)i <= slot;
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+    r += k * step;
+    left = min(step, left - k * step);
   }
-  const int first = __ldg(p.cu + lo), qlen = __ldg(p.cu + lo + 1) - first;
-  const int L = __ldg(p.seq_lens + lo);
+  const int first = __ldg(p.cu + r), qlen = __ldg(p.cu + r + 1) - first;
+  const int L = __ldg(p.seq_lens + r);
   if (qlen <= 0 || first < 0 || (int64_t)first + qlen > p.T) return;
   const int64_t p0 = (int64_t)L - qlen;             // position of the request's first new row
-  const int64_t nth = slot - (first / bt + 2 * (int64_t)lo);
+  const int64_t nth = slot - (first / bt + 2 * (int64_t)r);
   // blocks do not cross pages: bt divides page_size
   const int64_t a = max(p0, (int64_t)0);
   const int64_t block0 = (a / bt + nth) * bt;       // first token of this block
@@ -101,28 +108,43 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendP
   const int64_t begin = max(block0, a);
   const int n_new = (int)(min(block0 + bt, (int64_t)L) - begin);
   const int n_old = (int)(begin - block0);
-  const int64_t lp = block0 / p.page_size;
-  const int page = lp < p.max_pages ? __ldg(p.page_table + (int64_t)lo * p.pt_stride + lp) : -1;
+  const int64_t x_st = p.x_st[which];
+  const uint16_t* x = p.x[which] + (first + (begin - p0)) * x_st + h * p.x_sh[which] + lane * 8;
+  uint4 row[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (warp + i * APPEND_WARPS < n_new) row[i] = __ldg(reinterpret_cast<const uint4*>(x + (warp + i * APPEND_WARPS) * x_st));
+  const int lp = (int)block0 / p.page_size;
+  const int page = lp < p.max_pages ? __ldg(p.page_table + (int64_t)r * p.pt_stride + lp) : -1;
   if (page < 0 || page >= p.num_pages) return;      // no page: the tokens are dropped
-  const int in_page = (int)(block0 - lp * p.page_size);
-  const uint16_t* x = p.x[which] + (first + (begin - p0)) * p.x_st[which] + h * p.x_sh[which] + lane * 8;
+  const int in_page = (int)block0 - lp * p.page_size;
   uint8_t* rows = p.cache[which] + page * p.kv_page_stride + in_page * p.kv_row_stride + h * p.kv_head_stride + lane * 8;
   float* sc = p.scale[which] + page * p.sc_page_stride + (in_page / bt) * p.sc_block_stride + h;
-
-  float top = 0.f;
-  for (int i = warp; i < n_new; i += APPEND_WARPS) {
-    float f[8];
-    widen8<F16>(__ldg(reinterpret_cast<const uint4*>(x + i * p.x_st[which])), f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]) <= 3.4e38f ? fabsf(f[k]) : 0.f);
-  }
-  top = attn8::warp_max(top);
-  if (lane == 0) top_s[warp] = top;
   const float before = n_old > 0 ? *sc : 0.f;
-  __syncthreads();
+
+  // largest finite magnitude, as a 16-bit pattern of its type
+  uint32_t top = 0;
+  auto measure = [&](uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int w = 0; w < APPEND_WARPS; ++w) top = fmaxf(top, top_s[w]);
-  const float s = fmaxf(before, __uint_as_float((uint32_t)(scale_exponent(top) + 127) << 23));
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t m = w[k] & 0x7fff7fffu;
+      const uint32_t fin = __vcmpltu2(m, F16 ? 0x7c007c00u : 0x7f807f80u);
+      top = __vmaxu2(top, m & fin);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (warp + i * APPEND_WARPS < n_new) measure(row[i]);
+  for (int i = warp + HELD * APPEND_WARPS; i < n_new; i += APPEND_WARPS)
+    measure(__ldg(reinterpret_cast<const uint4*>(x + i * x_st)));
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+  if (lane == 0) top_s[warp] = attn8::widen2<F16>(top).x;
+  __syncthreads();
+  float amax = 0.f;
+#pragma unroll
+  for (int w = 0; w < APPEND_WARPS; ++w) amax = fmaxf(amax, top_s[w]);
+  const float s = fmaxf(before, __uint_as_float((uint32_t)(scale_exponent(amax) + 127) << 23));
   if (threadIdx.x == 0 && s != before) *sc = s;
   if (n_old > 0 && s != before) {
     const float ratio = before / s;
@@ -137,13 +159,22 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendP
       *at = encode8(f);
     }
   }
-  for (int i = warp; i < n_new; i += APPEND_WARPS) {
+  // x / s: a power of two's reciprocal is exact; a scale of another writer's is divided by
+  const uint32_t sb = __float_as_uint(s);
+  const bool pow2 = (sb & 0x7fffffu) == 0 && sb > 0 && sb < 0x7e800000u;
+  const float inv = 1.f / s;
+  auto store = [&](int i, uint4 v) {
     float f[8];
-    widen8<F16>(__ldg(reinterpret_cast<const uint4*>(x + i * p.x_st[which])), f);
+    widen8<F16>(v, f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = f[k] / s;
+    for (int k = 0; k < 8; ++k) f[k] = pow2 ? f[k] * inv : f[k] / s;
     *reinterpret_cast<uint2*>(rows + (int64_t)(n_old + i) * p.kv_row_stride) = encode8(f);
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (warp + i * APPEND_WARPS < n_new) store(warp + i * APPEND_WARPS, row[i]);
+  for (int i = warp + HELD * APPEND_WARPS; i < n_new; i += APPEND_WARPS)
+    store(i, __ldg(reinterpret_cast<const uint4*>(x + i * x_st)));
   if (p.token_weight && h == 0 && which == 0)
     for (int i = threadIdx.x; i < n_new; i += blockDim.x)
       p.token_weight[(int64_t)page * p.page_size + in_page + n_old + i] = 0;
@@ -168,21 +199,22 @@ struct AccumulateParams {
   int32_t R;
   unsigned long long* token_weight;
   int32_t chunks;             // warps per row
+  attn8::FastDiv by_page;
 };
 
-constexpr int ACC_PER_WARP = 128;
 constexpr float ACC_MOST = 1048576.f;   // one weight counts at most 2^20
 
+template <int PER>   // list entries a lane
 __global__ void __launch_bounds__(256) accumulate_kernel(const AccumulateParams p) {
   const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (wid >= p.T * p.chunks) return;
   const int64_t t = wid / p.chunks;
-  const int e0 = (int)(wid % p.chunks) * ACC_PER_WARP + lane;
-  int j[ACC_PER_WARP / 32];
-  float w[ACC_PER_WARP / 32];
+  const int e0 = (int)(wid % p.chunks) * (32 * PER) + lane;
+  int j[PER];
+  float w[PER];
 #pragma unroll
-  for (int i = 0; i < ACC_PER_WARP / 32; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int e = e0 + 32 * i;
     j[i] = e < p.width ? __ldg(p.tok + t * p.tok_stride + e) : -1;
     w[i] = e < p.width ? __ldg(p.weights + t * p.w_stride + e) : 0.f;
@@ -190,16 +222,20 @@ __global__ void __launch_bounds__(256) accumulate_kernel(const AccumulateParams 
   int r, pos, L;
   attn8::row_position(p.cu, p.seq_lens, p.R, t, lane, r, pos, L);
   const int32_t* pt_row = p.page_table + (int64_t)r * p.pt_stride;
+  int page[PER];
 #pragma unroll
-  for (int i = 0; i < ACC_PER_WARP / 32; ++i) {
+  for (int i = 0; i < PER; ++i) {
     // NaN and weights at or below 0 add nothing
-    if (j[i] < 0 || j[i] > pos || j[i] >= L || !(w[i] > 0.f)) continue;
-    const int lp = j[i] / p.page_size;
-    const int page = lp < p.max_pages ? __ldg(pt_row + lp) : -1;
-    if (page < 0 || page >= p.num_pages) continue;
+    const bool adds = j[i] >= 0 && j[i] <= pos && j[i] < L && w[i] > 0.f;
+    const int lp = adds ? attn8::divide(j[i], p.by_page) : 0;
+    page[i] = adds && lp < p.max_pages ? __ldg(pt_row + lp) : -1;
+    j[i] -= lp * p.page_size;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (page[i] < 0 || page[i] >= p.num_pages) continue;
     const double units = (double)fminf(w[i], ACC_MOST) * 4294967296.0;
-    atomicAdd(p.token_weight + (int64_t)page * p.page_size + (j[i] - lp * p.page_size),
-              (unsigned long long)__double2ll_rn(units));
+    atomicAdd(p.token_weight + (int64_t)page[i] * p.page_size + j[i], (unsigned long long)__double2ll_rn(units));
   }
 }
 
@@ -229,25 +265,60 @@ __device__ __forceinline__ int logical_pages(const EvictParams& p, int r) {
   return L <= 0 ? 0 : (int)min((int64_t)p.max_pages, ((int64_t)L + p.page_size - 1) / p.page_size);
 }
 
-__global__ void __launch_bounds__(256) page_weight_kernel(const EvictParams p) {
-  const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (wid >= (int64_t)p.R * p.max_pages) return;
-  const int r = (int)(wid / p.max_pages), lp = (int)(wid % p.max_pages);
-  if (lp >= logical_pages(p, r)) return;
-  const int page = __ldg(p.page_table + (int64_t)r * p.pt_stride + lp);
-  if (page < 0 || page >= p.num_pages) return;
-  unsigned long long sum = 0;
-  const int64_t* w = p.token_weight + (int64_t)page * p.page_size;
-  for (int i = lane; i < p.page_size; i += 32) sum += (unsigned long long)__ldg(reinterpret_cast<const long long*>(w + i));
+// Page weights: `lanes` lanes (a power of two) sum a page, two tokens a load
+// where rows allow it; every group of lanes takes WEIGH_EACH logical pages of one
+// request, all in flight at once.
+constexpr int WEIGH_THREADS = 128, WEIGH_EACH = 8;
+
+template <bool PAIRS>
+__global__ void __launch_bounds__(WEIGH_THREADS) page_weight_kernel(const EvictParams p, int lanes) {
+  __shared__ int page_s[WEIGH_THREADS * WEIGH_EACH];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int sub = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = WEIGH_THREADS / lanes;
+  const int r = blockIdx.y, base = blockIdx.x * groups * WEIGH_EACH, n = logical_pages(p, r);
+  if (base >= n) return;
+  for (int i = threadIdx.x; i < groups * WEIGH_EACH; i += WEIGH_THREADS) {
+    const int page = base + i < n ? __ldg(p.page_table + (int64_t)r * p.pt_stride + base + i) : -1;
+    page_s[i] = page < p.num_pages ? page : -1;
+  }
+  __syncthreads();
+  unsigned long long sum[WEIGH_EACH];
+  const int64_t* w[WEIGH_EACH];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) p.key[wid] = sum ^ (1ull << 63);
+  for (int b = 0; b < WEIGH_EACH; ++b) {
+    const int page = page_s[b * groups + group];
+    sum[b] = 0;
+    w[b] = page < 0 ? nullptr : p.token_weight + (int64_t)page * p.page_size;
+  }
+  constexpr int STEP = PAIRS ? 2 : 1;
+  for (int e = STEP * sub; e < p.page_size; e += STEP * lanes) {
+#pragma unroll
+    for (int b = 0; b < WEIGH_EACH; ++b) {
+      if (!w[b]) continue;
+      if (PAIRS) {
+        const ulonglong2 v = __ldg(reinterpret_cast<const ulonglong2*>(w[b] + e));
+        sum[b] += v.x + v.y;
+      } else {
+        sum[b] += __ldg(reinterpret_cast<const unsigned long long*>(w[b] + e));
+      }
+    }
+  }
+  unsigned long long* key = p.key + (int64_t)r * p.max_pages + base;
+#pragma unroll
+  for (int b = 0; b < WEIGH_EACH; ++b) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], o);
+    if (sub == 0 && w[b]) key[b * groups + group] = sum[b] ^ (1ull << 63);
+  }
 }
 
-constexpr int EVICT_THREADS = 1024;
+// Selection: one CTA per request; a thread holds PER consecutive pages in
+// registers (PER * EVICT_THREADS >= max_pages) or, for longer tables (PER = 0),
+// looks them up again in every pass.
+constexpr int EVICT_THREADS = 512;
+constexpr int BINS = 512;                              // of a pass: 9 bits
+constexpr int PASSES = 8;                              // the first and up to 61 open bits after it
 
-// Sum over the CTA of one int per thread, and the exclusive prefix.
+// Exclusive prefix over the CTA of one int per thread, and the total.
 __device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int inc = v;
@@ -256,84 +327,217 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
     const int y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  __syncthreads();
+  __syncthreads();                                     // warp_s may still be read
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < EVICT_THREADS / 32; ++w) {
-    const int y = warp_s[w];
-    if (w < warp) before += y;
-    total += y;
+  constexpr int WARPS = EVICT_THREADS / 32;
+  int ws = lane < WARPS ? warp_s[lane] : 0, wi = ws;   // every warp scans the warp sums
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, wi, o);
+    if (lane >= o) wi += y;
   }
-  return before + inc - v;
+  total = __shfl_sync(0xffffffffu, wi, 31);
+  return __shfl_sync(0xffffffffu, wi - ws, warp) + inc - v;
 }
 
+template <int PER>
 __global__ void __launch_bounds__(EVICT_THREADS) evict_kernel(const EvictParams p) {
   __shared__ int warp_s[EVICT_THREADS / 32];
-  __shared__ int hist[256];
-  __shared__ unsigned long long prefix_s;
-  __shared__ int want_s;
-  const int r = blockIdx.x, tid = threadIdx.x;
+  __shared__ int hist_s[PASSES][BINS];
+  __shared__ unsigned long long and_s, or_s;
+  __shared__ int held_s, free_s, bin_s, left_s;
+  const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = logical_pages(p, r);
   const int32_t* row = p.page_table + (int64_t)r * p.pt_stride;
   int32_t* out = p.table_out + (int64_t)r * p.out_stride;
   int32_t* freed = p.freed + (int64_t)r * p.freed_stride;
-  const unsigned long long* key = p.key + (int64_t)r * p.max_pages;
-  auto live = [&](int lp) { return lp < n && row[lp] >= 0 && row[lp] < p.num_pages; };
-  auto held = [&](int lp) { return lp < p.keep_first || lp >= n - p.keep_last; };
+  const unsigned long long* keys = p.key + (int64_t)r * p.max_pages;
+  const int want_keep = __ldg(p.keep + r);
+  auto is_live = [&](int lp, int entry) { return lp < n && entry >= 0 && entry < p.num_pages; };
+  auto is_held = [&](int lp) { return lp < p.keep_first || lp >= n - p.keep_last; };
 
+  constexpr int HOLD = PER > 0 ? PER : 1;
+  int entry[HOLD];
+  unsigned long long key[HOLD];
+  bool may[HOLD];                                      // live and not held: may be dropped
   int n_held = 0, n_free = 0;
-  for (int lp = tid; lp < n; lp += EVICT_THREADS)
-    if (live(lp)) (held(lp) ? n_held : n_free)++;
-  int all_held, all_free;
-  block_prefix(n_held, warp_s, all_held);
-  block_prefix(n_free, warp_s, all_free);
-  const int quota = max(0, min(all_free, (int)__ldg(p.keep + r) - all_held));  // pages that may stay
+  if (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      const int lp = tid * HOLD + i;
+      entry[i] = lp < p.max_pages ? row[lp] : -1;
+      const bool live = is_live(lp, entry[i]);
+      may[i] = live && !is_held(lp);
+      n_held += live && !may[i];
+      n_free += may[i];
+    }
+  } else {
+    for (int lp = tid; lp < n; lp += EVICT_THREADS)
+      if (is_live(lp, row[lp])) (is_held(lp) ? n_held : n_free)++;
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) hist_s[i][tid] = 0;
+  if (tid == 0) {
+    and_s = ~0ull;
+    or_s = 0;
+    held_s = free_s = 0;
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the page weights
+  if (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) key[i] = may[i] ? keys[tid * HOLD + i] : 0;
+  }
+  // every droppable page's key, in no particular order
+  auto each_key = [&](auto&& f) {
+    if (PER > 0) {
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i)
+        if (may[i]) f(key[i]);
+    } else {
+      for (int lp = tid; lp < n; lp += EVICT_THREADS)
+        if (is_live(lp, row[lp]) && !is_held(lp)) f(keys[lp]);
+    }
+  };
+  unsigned long long all_and = ~0ull, all_or = 0;
+  each_key([&](unsigned long long k) {
+    all_and &= k;
+    all_or |= k;
+  });
+  n_held = __reduce_add_sync(0xffffffffu, n_held);
+  n_free = __reduce_add_sync(0xffffffffu, n_free);
+  const uint32_t and_lo = __reduce_and_sync(0xffffffffu, (uint32_t)all_and);
+  const uint32_t and_hi = __reduce_and_sync(0xffffffffu, (uint32_t)(all_and >> 32));
+  const uint32_t or_lo = __reduce_or_sync(0xffffffffu, (uint32_t)all_or);
+  const uint32_t or_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(all_or >> 32));
+  if (lane == 0) {
+    if (n_held) atomicAdd(&held_s, n_held);
+    if (n_free) {
+      atomicAdd(&free_s, n_free);
+      atomicAnd(&and_s, ((unsigned long long)and_hi << 32) | and_lo);
+      atomicOr(&or_s, ((unsigned long long)or_hi << 32) | or_lo);
+    }
+  }
+  __syncthreads();
+  const int all_free = free_s;
+  const int quota = max(0, min(all_free, want_keep - held_s));     // droppable pages that stay
+  const bool some = quota > 0 && quota < all_free;
 
-  // the quota-th largest key: its value and how many equal to it stay
+  // The quota-th largest key: pages stay when key & mask > prefix, and the first `want` pages when they are equal.
   unsigned long long prefix = 0, mask = 0;
   int want = quota;
-  if (quota > 0 && quota < all_free) {
-    for (int shift = 56; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+  bool whole = true;                                   // every page at the threshold stays
+  if (some) {
+    // leading bits in which all keys agree need no pass
+    const unsigned long long differ = and_s ^ or_s;
+    int top = differ ? 64 - __clzll((long long)differ) : 0;   // bits below `top` are open
+    mask = top >= 64 ? 0 : ~0ull << top;
+    prefix = and_s & mask;
+    whole = top > 0;                                   // all keys equal: the first ones stay
+    // Histogram of the keys that share the prefix, then the bin of the want-th largest (bin_s), how many of it stay.
+    auto find = [&](int* hist, auto&& bin_of) {
+      each_key([&](unsigned long long k) {
+        if ((k & mask) == prefix) atomicAdd(&hist[bin_of(k)], 1);
+      });
       __syncthreads();
-      for (int lp = tid; lp < n; lp += EVICT_THREADS)
-        if (live(lp) && !held(lp) && (key[lp] & mask) == prefix) atomicAdd(&hist[(key[lp] >> shift) & 255], 1);
-      __syncthreads();
-      if (tid == 0) {
-        int b = 255, left = want;
-        while (b > 0 && hist[b] < left) left -= hist[b--];
-        prefix_s = prefix | ((unsigned long long)b << shift);
-        want_s = left;
+      if (warp == 0) {
+        // lane l sums bins 16 (31 - l) .. + 15, so that a prefix over lanes counts from the largest bin down
+        const int b0 = BINS / 32 * (31 - lane);
+        int sum = 0;
+#pragma unroll
+        for (int b = 0; b < BINS / 32; ++b) sum += hist[b0 + b];
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        if (inc >= want && inc - sum < want) {         // the threshold's bin is among this lane's
+          int left = want - (inc - sum), b = BINS / 32 - 1;
+          while (b > 0 && hist[b0 + b] < left) left -= hist[b0 + b--];
+          bin_s = b0 + b;
+          left_s = left;
+        }
       }
       __syncthreads();
-      prefix = prefix_s;
-      want = want_s;
-      mask |= 255ull << shift;
+      want = left_s;
+      whole = hist[bin_s] == want;
+      return bin_s;
+    };
+    // First by the highest bit that differs and the 3 below it: weights spread over many powers of two, and bins of
+    // equal width would put most of them (and their atomics) in one.
+    int pass = 0;
+    if (top > 0) {
+      const unsigned long long low = top >= 64 ? ~0ull : (1ull << top) - 1;
+      const int b = find(hist_s[pass++], [&](unsigned long long k) {
+        const unsigned long long v = k & low;
+        const int m = 63 - __clzll((long long)(v | 1));
+        return m < 3 ? (int)v : 8 * (m - 2) + (int)((v >> (m - 3)) & 7);
+      });
+      top = b < 8 ? 0 : b / 8 - 1;                     // bits still open: below m - 3, m = b / 8 + 2
+      prefix |= b < 8 ? (unsigned long long)b : (unsigned long long)(8 + (b & 7)) << top;
+      mask = ~0ull << top;
+    }
+    while (top > 0 && !whole) {
+      const int bits = min(9, top), shift = top - bits;
+      __syncthreads();                                 // bin_s and left_s are read
+      const int b = find(hist_s[pass++], [&](unsigned long long k) { return (int)(k >> shift) & ((1 << bits) - 1); });
+      prefix |= (unsigned long long)b << shift;
+      mask |= ((1ull << bits) - 1) << shift;
+      top = shift;
     }
   }
-  // in page order: the first `want` pages at the threshold stay, then the new table and the freed list
-  int ties = 0, gone = 0;
-  for (int base = 0; base < p.max_pages; base += EVICT_THREADS) {
-    const int lp = base + tid;
-    const int entry = lp < p.max_pages ? row[lp] : -1;
-    const bool may = lp < p.max_pages && live(lp) && !held(lp);
-    const unsigned long long k = may ? key[lp] : 0;
-    const bool tie = may && quota > 0 && quota < all_free && k == prefix;
-    int total;
-    const int at = ties + block_prefix(tie ? 1 : 0, warp_s, total);
-    ties += total;
-    const bool stays = !may || quota >= all_free || (quota > 0 && (k > prefix || (tie && at < want)));
-    const int to = gone + block_prefix(stays ? 0 : 1, warp_s, total);
-    gone += total;
-    if (lp < p.max_pages) {
-      out[lp] = stays ? entry : -1;
-      if (!stays) freed[to] = entry;
+  if (PER > 0) {
+    int rank = 0, total;
+    if (!whole) {                                      // the tied pages' order decides
+      int ties = 0;
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) ties += may[i] && (key[i] & mask) == prefix;
+      rank = block_prefix(ties, warp_s, total);
     }
+    bool stays[HOLD];
+    int gone = 0;
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      const unsigned long long k = key[i] & mask;
+      const bool tie = may[i] && k == prefix;
+      stays[i] = !may[i] || quota >= all_free || (some && (k > prefix || (tie && (whole || rank < want))));
+      rank += tie;
+      gone += !stays[i];
+    }
+    int at = block_prefix(gone, warp_s, total);
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      const int lp = tid * HOLD + i;
+      if (lp >= p.max_pages) break;
+      out[lp] = stays[i] ? entry[i] : -1;
+      if (!stays[i]) freed[at++] = entry[i];
+    }
+    for (int i = total + tid; i < p.max_pages; i += EVICT_THREADS) freed[i] = -1;
+    if (tid == 0) p.counts[r] = total;
+  } else {
+    int ties = 0, gone = 0;
+    for (int base = 0; base < p.max_pages; base += EVICT_THREADS) {
+      const int lp = base + tid;
+      const int e = lp < p.max_pages ? row[lp] : -1;
+      const bool drop = is_live(lp, e) && !is_held(lp);
+      const unsigned long long k = drop ? keys[lp] & mask : 0;
+      const bool tie = some && drop && k == prefix;
+      int total;
+      const int rank = ties + block_prefix(tie ? 1 : 0, warp_s, total);
+      ties += total;
+      const bool stays = !drop || quota >= all_free || (some && (k > prefix || (tie && rank < want)));
+      const int to = gone + block_prefix(stays ? 0 : 1, warp_s, total);
+      gone += total;
+      if (lp < p.max_pages) {
+        out[lp] = stays ? e : -1;
+        if (!stays) freed[to] = e;
+      }
+    }
+    for (int i = gone + tid; i < p.max_pages; i += EVICT_THREADS) freed[i] = -1;
+    if (tid == 0) p.counts[r] = gone;
   }
-  for (int i = gone + tid; i < p.max_pages; i += EVICT_THREADS) freed[i] = -1;
-  if (tid == 0) p.counts[r] = gone;
 }
 
 }  // namespace kv8

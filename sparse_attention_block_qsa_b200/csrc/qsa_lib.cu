@@ -1453,7 +1453,9 @@ qsa_status_t qsa_accumulate_weights(const float* weights, int64_t weights_stride
         overlaps(rt, span(token_idx, 4, T, T > 1 ? tok_stride : 0, 1, 0, 1, 0, width)))
       return fail(QSA_ERR_INVALID_ARG, "token_weight overlaps an input");
   }
-  const int32_t chunks = (width - 1) / qsa::kv8::ACC_PER_WARP + 1;
+  // entries a lane: few while the warps fit the GPU at once (148 SMs x 64), more when there are several rounds of them
+  const int per = T * ((width + 127) / 128) <= 2 * 9472 ? 4 : 8;
+  const int32_t chunks = (width - 1) / (32 * per) + 1;
   const int64_t blocks = (T * chunks * 32 + 255) / 256;
   if (blocks > INT32_MAX) return fail(QSA_ERR_UNSUPPORTED, "too many entries for one launch");
   int sms = 0;
@@ -1476,7 +1478,10 @@ qsa_status_t qsa_accumulate_weights(const float* weights, int64_t weights_stride
   p.R = R;
   p.token_weight = reinterpret_cast<unsigned long long*>(token_weight);
   p.chunks = chunks;
-  qsa::kv8::accumulate_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  p.by_page = qsa::attn8::fast_div((uint32_t)page_size);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (per == 4) qsa::kv8::accumulate_kernel<4><<<(unsigned)blocks, 256, 0, s>>>(p);
+  else qsa::kv8::accumulate_kernel<8><<<(unsigned)blocks, 256, 0, s>>>(p);
   return launch_status("weight accumulation kernel");
 }
 
@@ -1513,8 +1518,6 @@ qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int
       return fail(QSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace_bytes, need);
     if (!aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   }
-  const int64_t pages = (int64_t)R * max_pages;
-  if ((pages * 32 + 255) / 256 > INT32_MAX) return fail(QSA_ERR_UNSUPPORTED, "too many pages for one launch");
   int sms = 0;
   st = device_info(&sms);
   if (st != QSA_OK) return st;
@@ -1537,8 +1540,37 @@ qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int
   p.counts = counts;
   p.key = static_cast<unsigned long long*>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pages > 0) qsa::kv8::page_weight_kernel<<<(unsigned)((pages * 32 + 255) / 256), 256, 0, s>>>(p);
-  qsa::kv8::evict_kernel<<<(unsigned)R, qsa::kv8::EVICT_THREADS, 0, s>>>(p);
+  // lanes that sum a page: two tokens a load where every page's row is 16-byte aligned
+  const bool pairs = page_size % 2 == 0 && aligned(token_weight, 16);
+  int lanes = 1;
+  while (lanes < 32 && lanes * (pairs ? 2 : 1) < page_size) lanes *= 2;
+  const int32_t span_pages = qsa::kv8::WEIGH_THREADS / lanes * qsa::kv8::WEIGH_EACH;
+  const unsigned spans = (unsigned)(((int64_t)max_pages + span_pages - 1) / span_pages);
+  for (int32_t r0 = 0; r0 < R; r0 += 65535) {            // requests in grid y
+    const int32_t rows = std::min(R - r0, 65535);
+    qsa::kv8::EvictParams q = p;
+    q.page_table += (max_pages > 0) ? (int64_t)r0 * q.pt_stride : 0;
+    q.seq_lens += r0;
+    q.keep += r0;
+    q.R = rows;
+    if (max_pages > 0) {
+      q.table_out += (int64_t)r0 * q.out_stride;
+      q.freed += (int64_t)r0 * q.freed_stride;
+      q.key += (int64_t)r0 * max_pages;
+    }
+    q.counts += r0;
+    const dim3 grid(spans, (unsigned)rows);
+    if (spans > 0) {
+      if (pairs) qsa::kv8::page_weight_kernel<true><<<grid, qsa::kv8::WEIGH_THREADS, 0, s>>>(q, lanes);
+      else qsa::kv8::page_weight_kernel<false><<<grid, qsa::kv8::WEIGH_THREADS, 0, s>>>(q, lanes);
+    }
+    const dim3 one((unsigned)rows), threads(qsa::kv8::EVICT_THREADS);
+    if (max_pages <= qsa::kv8::EVICT_THREADS) launch_pdl(qsa::kv8::evict_kernel<1>, one, threads, 0, s, q);
+    else if (max_pages <= 2 * qsa::kv8::EVICT_THREADS) launch_pdl(qsa::kv8::evict_kernel<2>, one, threads, 0, s, q);
+    else if (max_pages <= 4 * qsa::kv8::EVICT_THREADS) launch_pdl(qsa::kv8::evict_kernel<4>, one, threads, 0, s, q);
+    else if (max_pages <= 8 * qsa::kv8::EVICT_THREADS) launch_pdl(qsa::kv8::evict_kernel<8>, one, threads, 0, s, q);
+    else launch_pdl(qsa::kv8::evict_kernel<0>, one, threads, 0, s, q);
+  }
   return launch_status("page eviction kernels");
 }
 
