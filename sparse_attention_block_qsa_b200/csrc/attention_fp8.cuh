@@ -17,13 +17,14 @@
 //    fp16 one, down to an absolute 2^-22 of the head's largest element.
 //  * The output is O^T = V^T P: the V rows stay [entry][feature] in shared
 //    memory and are read as an M-major operand (M = 128 features, two
-//    halves), P as an N-major one, so thread e writes its 16 heads of a term
-//    as one 16-byte store.  P (times v_scale_j over the tile's largest
-//    v_scale, so at most 1) is split into three terms the same way: 2^-12
-//    relative, 2^-26 of the tile's largest, well below the 16-bit output's
-//    rounding.
-//  * Running maximum, sum and output are fp32 in registers (thread = feature
-//    for the output); each tile's O^T is read back from TMEM and added.
+//    halves), P as an N-major one, so that a thread writes its heads' codes in
+//    16-byte stores.  P (times v_scale_j over a reference v_scale) is split into
+//    four terms the same way: 2^-16 relative, 2^-22 of the reference, well below
+//    the 16-bit output's rounding.  Four, not three, because the reference below
+//    may lag by 2^6 and 7; the N columns of 8 or 12 heads, a multiple of 16, have
+//    room for them anyway.
+//  * Sums over entries are fp32: of the probabilities in registers, of the
+//    output in TMEM and, when the reference moves, in registers.
 //
 // Work is the list of (row, KV head, 128-entry tile) triples in order; every CTA
 // takes an equal contiguous run of it (two CTAs per SM), so any batch fills the
@@ -39,7 +40,7 @@
 //  * warps 9-11 split each new row's queries;
 //  * warps 0-3 run the softmax (thread = entry, then feature).  Scores are taken
 //    relative to a reference maximum that moves only when a tile exceeds it by
-//    2^3 (or its v_scale by a factor of 3.5): until then a tile needs no reduction,
+//    2^6 (or its v_scale by a factor of 7): until then a tile needs no reduction,
 //    only a vote, and its output product adds up in TMEM.
 #pragma once
 
@@ -62,15 +63,16 @@ constexpr int THREADS = SOFT + PROD + 128;   // the last warpgroup: MMA issue, q
 constexpr int REGS_LAUNCH = 80, REGS_SOFT = 152, REGS_PROD = 48, REGS_REST = 40;
 static_assert(REGS_SOFT + REGS_PROD + REGS_REST <= 3 * REGS_LAUNCH, "setmaxnreg would wait for ever");
 // A probability is at most 2^REF_SLACK times the reference and v_scale at most
-// V_SLACK times its own; times P_UNIT that is E4M3's largest value.
-constexpr float REF_SLACK = 3.f, V_SLACK = 3.5f, P_UNIT = 16.f;
+// V_SLACK times its own: together 448, E4M3's largest value.
+constexpr float REF_SLACK = 6.f, V_SLACK = 7.f;
 constexpr int MAX_GROUP = 16;          // query heads per KV head
-constexpr int PT = 3;                  // E4M3 terms of a probability
+constexpr int PT = 4;                  // E4M3 terms of a probability
 constexpr int BUFS = 3;
 constexpr int HALF_BYTES = TILE * 128;       // 128 features of every entry
 constexpr int BUF_BYTES = 2 * HALF_BYTES;
 constexpr int QC_SLOTS = 8;            // rows whose head factors are held: the current one and S_BUFS ahead fit
 constexpr int Q_WARPS = 3;
+constexpr size_t SMEM_OF_TWO = 233472 / 2 - 1024;   // dynamic shared memory of a CTA when two share an SM
 
 // Sizes of one instance: 16-bit type and query heads held per KV head.
 template <bool F16, int HG>
@@ -79,18 +81,19 @@ struct Cfg {
   static constexpr int QCOLS = QT * HG, QN = (QCOLS + 15) / 16 * 16, QROWS = (QCOLS + 7) / 8 * 8;
   static constexpr int PCOLS = PT * HG, PN = (PCOLS + 15) / 16 * 16;
   static constexpr int S_BUFS = F16 ? 3 : 4;                      // score tiles held in TMEM
-  static constexpr uint32_t TMEM = 256;                           // columns; two CTAs share 512
-  static_assert(S_BUFS * QN + 2 * PN <= TMEM, "TMEM columns");
+  static constexpr uint32_t TMEM = S_BUFS * QN + 2 * PN <= 256 ? 256 : 512;   // columns; two CTAs share 512
   static constexpr int Q_BYTES = QROWS * D;
   static constexpr int P_BYTES = PN * TILE;
   static constexpr int BARS = 2 * BUFS + 2 * S_BUFS + 5;
-  // Scales of two tiles in shared memory, copied with the K rows; where there is no room (fp16, 12 heads) the
-  // softmax threads look their entries up themselves.
-  static constexpr bool RING = !(F16 && HG == 12);
-  static constexpr int RING_BYTES = RING ? 2 * TILE * 8 : 0;
-  static constexpr size_t SMEM =
-      BUFS * BUF_BYTES + Q_BYTES + P_BYTES + RING_BYTES + BARS * 8 + 4 * 17 * 4 + QC_SLOTS * HG * 4 + 16;
-  static constexpr int RESIDENT = 2 * (SMEM + 1024) <= 233472 ? 2 : 1;   // CTAs per SM
+  // Scales of four tiles in shared memory, copied with the K rows, where two CTAs an SM leave room for them;
+  // elsewhere the softmax threads look their entries up themselves.
+  static constexpr size_t REST = BUFS * BUF_BYTES + Q_BYTES + P_BYTES + BARS * 8 + 4 * 17 * 4 + QC_SLOTS * HG * 4 + 16;
+  static constexpr int RING_TILES = 4;
+  static constexpr bool RING = REST + RING_TILES * TILE * 8 <= SMEM_OF_TWO;
+  static constexpr int RING_BYTES = RING ? RING_TILES * TILE * 8 : 0;
+  static constexpr size_t SMEM = REST + RING_BYTES;
+  static_assert(TMEM == 256 || SMEM > SMEM_OF_TWO, "two CTAs would wait for each other's TMEM");
+  static constexpr int RESIDENT = SMEM <= SMEM_OF_TWO ? 2 : 1;   // CTAs per SM
 };
 
 // n / d for 0 <= n < 2^31 as a product and a shift.
@@ -304,7 +307,7 @@ struct Feed {
   int entry, lane;
   int jA[E], lastA, gA;       // list entries loaded
   const int32_t* ptA;
-  int jB[E], pageB[E], gB;    // pages loaded
+  int jB[E], pageB[E], lastB, gB;   // pages loaded
 
   __device__ __forceinline__ void row(const Params& p) {
     int r, pos, L;
@@ -333,11 +336,12 @@ struct Feed {
   }
   __device__ __forceinline__ void load_pages(const Params& p) {
     gB = gA;
+    lastB = lastA;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      jB[i] = jA[i] <= lastA ? jA[i] : -1;
+      jB[i] = jA[i];
       pageB[i] = -1;
-      if (jB[i] >= 0) {
+      if (jB[i] >= 0) {                                // what the row may see is checked later: `last` may be in flight
         const int lp = divide(jB[i], p.by_page);
         if (lp < p.max_pages) pageB[i] = __ldg(ptA + lp);
       }
@@ -350,8 +354,15 @@ struct Feed {
     t = pair / p.Hkv;
     g = pair - t * p.Hkv;
     left = n;
+    // the first tile's list entries are on their way while the row is looked up
+    int first[E];
+    const int e = tile * TILE + entry;
+#pragma unroll
+    for (int i = 0; i < E; ++i) first[i] = e + i < p.width ? __ldg(p.tok + (int64_t)t * p.tok_stride + e + i) : -1;
     row(p);
     load_entries(p);
+#pragma unroll
+    for (int i = 0; i < E; ++i) jA[i] = first[i];
     load_pages(p);
     load_entries(p);
   }
@@ -361,7 +372,7 @@ struct Feed {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       j[i] = jB[i];
-      page[i] = (int64_t)pageB[i] < p.num_pages ? pageB[i] : -1;
+      page[i] = jB[i] <= lastB && (int64_t)pageB[i] < p.num_pages ? pageB[i] : -1;
     }
     load_pages(p);
     load_entries(p);
@@ -392,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
   uint8_t* buf_s = smem8;
   uint8_t* q_s = buf_s + BUFS * BUF_BYTES;             // [half][QROWS][128 bytes], swizzled; row = term * HG + head
   uint8_t* p_s = q_s + C::Q_BYTES;                     // [16 columns][entry][16 bytes]; column = term * HG + head
-  float* sc_s = reinterpret_cast<float*>(p_s + C::P_BYTES);   // [2][K, V][TILE] scales, 0 for unseen entries
+  float* sc_s = reinterpret_cast<float*>(p_s + C::P_BYTES);   // [RING_TILES][K, V][TILE] scales, 0 for unseen entries
   uint64_t* bars = reinterpret_cast<uint64_t*>(p_s + C::P_BYTES + C::RING_BYTES);
   uint64_t *kv_full = bars, *kv_empty = kv_full + BUFS, *s_full = kv_empty + BUFS, *s_empty = s_full + S_BUFS,
            *p_full = s_empty + S_BUFS, *o_full = p_full + 1, *q_full = o_full + 1, *q_empty = q_full + 1,
@@ -404,6 +415,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
   volatile int* add_s = abort + 1;                     // whether the next output product adds to what TMEM holds
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid's end
   const int u0 = run_begin(p, blockIdx.x), n = run_begin(p, blockIdx.x + 1) - u0;
   const int pair0 = u0 / p.tiles, tile0 = u0 - pair0 * p.tiles;
 
@@ -444,14 +456,16 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     const int u = lane & 15, row2 = lane >> 4;         // 16 lanes a row, two rows per instruction
     Feed<1> f;
     f.start(p, pair0, tile0, n, 32 * w + lane, lane);
-    // rows of the warp's 32 entries into buffer item % BUFS
-    auto gather = [&](const uint8_t* base, int row, int item, int64_t scale_at) -> bool {
+    // rows of the warp's 32 entries into the next buffer.  K goes one tile ahead of V: it is consumed as soon as it
+    // lands, V only after the softmax.
+    int item = 0;
+    auto gather = [&](const uint8_t* base, int row, int tile, int64_t scale_at) -> bool {
       const int b = item % BUFS;
       if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[b], (uint32_t)((item / BUFS) & 1) ^ 1, abort))) return false;
       const uint32_t dst = smem_addr(buf_s + b * BUF_BYTES) + (u >> 3) * HALF_BYTES + (32 * w + row2) * 128;
       const uint8_t* src = base + u * 16;
-      if (C::RING && (item & 1) == 0) {                // the tile's scales land with its K rows
-        const uint32_t at = smem_addr(sc_s + (item >> 1 & 1) * 2 * TILE + 32 * w + lane);
+      if (C::RING && scale_at >= 0) {                  // the tile's scales land with its K rows
+        const uint32_t at = smem_addr(sc_s + tile % C::RING_TILES * 2 * TILE + 32 * w + lane);
         cp_async4(at, p.k_scale + scale_at, row >= 0);
         cp_async4(at + TILE * 4, p.v_scale + scale_at, row >= 0);
       }
@@ -463,19 +477,22 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         attn::cp_async16(dst + i * 256 + (((u & 7) ^ ((2 * i + row2) & 7)) << 4),
                          src + (int64_t)max(rr[i], 0) * p.pitch, rr[i] >= 0);
       cp_async_arrive(&kv_full[b]);
+      ++item;
       return true;
     };
+    int row_v = -1;                                    // the last tile's row, whose V is still to come
+    bool ok = true;
     for (int k = 0; k < n; ++k) {
       int page[1], j[1], g;
       f.next(p, page, j, g);
       const int in_page = j[0] - divide(j[0], p.by_page) * p.page_size;
       const int row = page[0] < 0 ? -1 : page[0] * p.page_rows + in_page * p.token_rows + g * p.head_rows;
       const int64_t at = C::RING && row >= 0 ? scale_index(p, page[0], in_page, g) : 0;
-      if (!gather(p.k, row, 2 * k, at) || !gather(p.v, row, 2 * k + 1, 0)) {
-        gone();
-        break;
-      }
+      ok = gather(p.k, row, k, at) && (k == 0 || gather(p.v, row_v, k - 1, -1));
+      if (!ok) break;
+      row_v = row;
     }
+    if (!ok || !gather(p.v, row_v, n - 1, -1)) gone();
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 8) {
     if constexpr (C::RESIDENT > 1) regs_shrink<REGS_REST>();
@@ -485,8 +502,9 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     const uint64_t kv_desc = umma_desc_sw128(smem_addr(buf_s));
     const uint64_t p_desc = desc_plain_mn(smem_addr(p_s), 128, TILE * 16);
     int ks = 0, ko = 0;                                // next tile of either product
-    int kb = 0, vb = 1;                                // their buffers
-    uint32_t kp = 0, vp = 0;                           // and those buffers' phases
+    // K of tile k is item 2 k - 1 (0 for the first), V is item 2 k + 2 (2 n - 1 for the last)
+    auto k_item = [](int k) { return k == 0 ? 0 : 2 * k - 1; };
+    auto v_item = [&](int k) { return k + 1 < n ? 2 * k + 2 : 2 * n - 1; };
     int sb = 0;                                        // score buffer of ks and its phase
     uint32_t sp = 0;
     int tile = tile0, nth = 0;                         // of S: tile in its pair, pairs begun
@@ -495,6 +513,8 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     uint32_t idle = 0;
     while (ko < n) {
       bool did = false;
+      const int ki = k_item(ks), kb = ki % BUFS, vi = v_item(ko), vb = vi % BUFS;
+      const uint32_t kp = (uint32_t)(ki / BUFS) & 1, vp = (uint32_t)(vi / BUFS) & 1;
       if (ko < ks && __all_sync(0xffffffffu, mbar_test(p_full, (uint32_t)ko & 1) &&
                                                  mbar_test(&kv_full[vb], vp))) {
         fence_proxy_async_smem();                      // the cp.async writes, before the tensor core reads them
@@ -513,11 +533,6 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         }
         __syncwarp();
         ++ko;
-        vb += 2;
-        if (vb >= BUFS) {
-          vb -= BUFS;
-          vp ^= 1;
-        }
         did = true;
       }
       if (ks < n && ks < ko + S_BUFS &&
@@ -547,11 +562,6 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         if (++sb == S_BUFS) {
           sb = 0;
           sp ^= 1;
-        }
-        kb += 2;
-        if (kb >= BUFS) {
-          kb -= BUFS;
-          kp ^= 1;
         }
         did = true;
       }
@@ -661,7 +671,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       tc_fence_after();
     };
     auto take_output = [&]() {                         // o += what TMEM holds
-      const float2 unit = both(vref * (1.f / P_UNIT));
+      const float2 unit = both(vref);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         float d[(C::PCOLS + 7) / 8 * 8];
@@ -673,6 +683,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           float2 x = make_float2(d[2 * i], d[2 * i + 1]);
           x = fma2(make_float2(d[HG + 2 * i], d[HG + 2 * i + 1]), both(1.f / 16.f), x);
           x = fma2(make_float2(d[2 * HG + 2 * i], d[2 * HG + 2 * i + 1]), both(1.f / 256.f), x);
+          x = fma2(make_float2(d[3 * HG + 2 * i], d[3 * HG + 2 * i + 1]), both(1.f / 4096.f), x);
           o[i] = fma2(x, unit, o[i]);
         }
       }
@@ -685,7 +696,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         if (!mbar_wait(&s_full[sb], sp, abort)) gone();
         tc_fence_after();
         if constexpr (C::RING) {
-          const float* sc = sc_s + (k & 1) * 2 * TILE + tid;
+          const float* sc = sc_s + k % C::RING_TILES * 2 * TILE + tid;
           ks = sc[0];
           vs = sc[TILE];
           seen = ks != 0.f;
@@ -776,7 +787,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       }
       if constexpr (!C::RING) scales();                // of tile k + 1
       // ---- P times v_scale / vref as three E4M3 terms
-      const float2 vn = both(vs * vinv * P_UNIT);
+      const float2 vn = both(vs * vinv);
       uint32_t w4[PN / 4];
 #pragma unroll
       for (int i = 0; i < PN / 4; ++i) w4[i] = 0;
@@ -813,8 +824,6 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       fresh = ++tile == p.tiles;
       if (fresh || k + 1 == n) {
         // ---- end of the pair or of the run: output, or the piece for the merge
-        output_done(k);
-        take_output();
         const bool whole = fresh && k + 1 >= p.tiles;
         float mine = 0.f, mref_lane = 0.f;             // of head `lane`
 #pragma unroll
@@ -834,6 +843,8 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         named_barrier_sync(2, SOFT);
         const int64_t t = pair / p.Hkv;
         const int g = pair - (int)t * p.Hkv;
+        output_done(k);                                // (the product ran under the sums above)
+        take_output();
         if (whole) {
           float mul = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
           const int64_t hq = t * p.Hq + (int64_t)g * p.group;
@@ -877,7 +888,6 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
   }
   tc_fence_before();
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 8) tmem_dealloc(tmem, C::TMEM);
 }
 
