@@ -633,7 +633,7 @@ def sparse_attention_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
             raise ValueError("weights must be fp32 [T, width] with unit column stride")
         weights_p = weights.data_ptr()
     if out is None:
-        out = _new(stream, (T, Hq, 256), dt, dev)
+        out = torch.empty_like(q) if stream is None and q.is_contiguous() else _new(stream, (T, Hq, 256), dt, dev)
         out0 = Hq * 256
     else:
         _want(out, "out", dt, 3, dev)

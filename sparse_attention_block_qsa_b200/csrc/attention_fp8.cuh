@@ -121,7 +121,7 @@ struct Params {
   FastDiv by_page, by_block;  // / page_size, / block_tokens
   // Strides of the cache in rows of `pitch` bytes, the greatest common divisor
   // of the byte strides: a row's place is a 32-bit number.
-  int64_t pitch;
+  uint32_t pitch;
   int32_t page_rows, token_rows, head_rows;
   int64_t sc_page_stride, sc_block_stride;                // elements
   const int32_t* page_table;
@@ -215,6 +215,9 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 2^-inf = 0
 
 // Arrives on bar once this thread's cp.async copies so far have landed; the
 // barrier counts this arrival like any other.
+__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
@@ -472,10 +475,15 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       int rr[16];                                      // all the look-ups before the copies
 #pragma unroll
       for (int i = 0; i < 16; ++i) rr[i] = __shfl_sync(0xffffffffu, row, 2 * i + row2);
+      auto place = [&](int i) { return dst + i * 256 + (((u & 7) ^ ((2 * i + row2) & 7)) << 4); };
+      if (__all_sync(0xffffffffu, row >= 0)) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        attn::cp_async16(dst + i * 256 + (((u & 7) ^ ((2 * i + row2) & 7)) << 4),
-                         src + (int64_t)max(rr[i], 0) * p.pitch, rr[i] >= 0);
+        for (int i = 0; i < 16; ++i) cp_async16_all(place(i), src + (uint64_t)(uint32_t)rr[i] * p.pitch);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          attn::cp_async16(place(i), src + (uint64_t)(uint32_t)max(rr[i], 0) * p.pitch, rr[i] >= 0);
+      }
       cp_async_arrive(&kv_full[b]);
       ++item;
       return true;
@@ -645,7 +653,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     if constexpr (!C::RING) f.start(p, pair0, tile0, n, tid, lane);
     // heads 2 i, 2 i + 1: sums over this thread's entries; features tid and 128 + tid
     float2 l_run[HG / 2], o0[HG / 2], o1[HG / 2];
-    float mref[HG];                                    // same in every thread
+    float2 nref[HG / 2];                               // the references, negated; same in every thread
     float vref = 0.f, vinv = 0.f;
     bool set = false;                                  // mref holds maxima: a tile had a visible entry
     bool add = false;                                  // TMEM holds output of this pair that o0, o1 lack
@@ -703,9 +711,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         }
         if (fresh) {
 #pragma unroll
-          for (int h = 0; h < HG; ++h) mref[h] = 0.f;
-#pragma unroll
-          for (int i = 0; i < HG / 2; ++i) l_run[i] = o0[i] = o1[i] = make_float2(0.f, 0.f);
+          for (int i = 0; i < HG / 2; ++i) nref[i] = l_run[i] = o0[i] = o1[i] = make_float2(0.f, 0.f);
           vref = vinv = 0.f;
           add = set = false;
         }
@@ -724,8 +730,12 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           x[i] = fma2(make_float2(d[HG + 2 * i], d[HG + 2 * i + 1]), both(1.f / 16.f), make_float2(d[2 * i], d[2 * i + 1]));
           if (QT > 2)
             x[i] = fma2(make_float2(d[(QT - 1) * HG + 2 * i], d[(QT - 1) * HG + 2 * i + 1]), both(1.f / 256.f), x[i]);
-          x[i] = mul2(x[i], mul2(qc[i], both(ks)));
-          if (!seen) x[i] = make_float2(-INFINITY, -INFINITY);
+          x[i] = fma2(x[i], mul2(qc[i], both(ks)), nref[i]);
+        }
+        if (!__all_sync(0xffffffffu, seen)) {
+#pragma unroll
+          for (int i = 0; i < HG / 2; ++i)
+            if (!seen) x[i] = make_float2(-INFINITY, -INFINITY);
         }
       }
       if (p.part_s) {
@@ -734,13 +744,12 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           float* dst = p.part_s + ((int64_t)pair * p.width + e) * p.group;
 #pragma unroll
           for (int h = 0; h < HG; ++h)
-            if (h < p.group) dst[h] = h & 1 ? x[h / 2].y : x[h / 2].x;
+            if (h < p.group) dst[h] = h & 1 ? x[h / 2].y - nref[h / 2].y : x[h / 2].x - nref[h / 2].x;
         }
       }
       float over = -INFINITY;
 #pragma unroll
       for (int i = 0; i < HG / 2; ++i) {
-        x[i] = add2(x[i], make_float2(-mref[2 * i], -mref[2 * i + 1]));
         over = fmaxf(over, fmaxf(x[i].x, x[i].y));
       }
       if (barrier_any(1, SOFT, !set || over > REF_SLACK || vs > V_SLACK * vref)) {
@@ -748,7 +757,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         float mine = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HG; ++h) {
-          const float wm = warp_max((h & 1 ? x[h / 2].y : x[h / 2].x) + mref[h]);
+          const float wm = warp_max(h & 1 ? x[h / 2].y - nref[h / 2].y : x[h / 2].x - nref[h / 2].x);
           if (lane == h) mine = wm;
         }
         const float vm = warp_max(vs);
@@ -765,17 +774,18 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         bool any = false;
 #pragma unroll
         for (int i = 0; i < HG / 2; ++i) {
-          float a[2];
+          float a[2], nr[2] = {nref[i].x, nref[i].y};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int h = 2 * i + e;
             float m = fmaxf(fmaxf(red_s[h], red_s[17 + h]), fmaxf(red_s[34 + h], red_s[51 + h]));
             any = any || m > -INFINITY;
-            if (set) m = fmaxf(m, mref[h]);
+            if (set) m = fmaxf(m, -nr[e]);
             if (!(m > -INFINITY)) m = 0.f;             // nothing visible yet (or only NaN)
-            a[e] = mref[h] - m;
-            mref[h] = m;
+            a[e] = -nr[e] - m;
+            nr[e] = -m;
           }
+          nref[i] = make_float2(nr[0], nr[1]);
           x[i] = add2(x[i], make_float2(a[0], a[1]));
           const float2 alpha = set ? make_float2(exp2_fast(a[0]), exp2_fast(a[1])) : both(1.f);
           l_run[i] = mul2(l_run[i], alpha);
@@ -833,7 +843,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
           if (lane == h) {
             mine = l;
-            mref_lane = mref[h];
+            mref_lane = h & 1 ? -nref[h / 2].y : -nref[h / 2].x;
           }
         }
         if (lane < 16) red_s[warp * 17 + lane] = mine;

@@ -1333,6 +1333,8 @@ static qsa_status_t attention_fp8_common(
                 head_stride = Hkv > 1 ? kv_head_stride : 0;
   int64_t pitch = std::gcd(std::gcd(page_stride, row_stride), head_stride);
   if (pitch == 0) pitch = D;
+  while (pitch > INT32_MAX && pitch % 2 == 0) pitch /= 2;
+  if (pitch > INT32_MAX) return fail(QSA_ERR_UNSUPPORTED, "cache strides out of range");
   const int64_t rows =
       ((num_pages - 1) * page_stride + (page_size - 1) * row_stride + (Hkv - 1) * head_stride) / pitch + 1;
   if (rows >= INT32_MAX)
@@ -1360,7 +1362,7 @@ static qsa_status_t attention_fp8_common(
   p.page_rows = (int32_t)(page_stride / pitch);
   p.token_rows = (int32_t)(row_stride / pitch);
   p.head_rows = (int32_t)(head_stride / pitch);
-  p.pitch = pitch;
+  p.pitch = (uint32_t)pitch;
   p.sc_page_stride = sc_page_stride;
   p.sc_block_stride = sc_block_stride;
   p.page_table = page_table;
