@@ -135,8 +135,8 @@ struct Params {
   int32_t width;
   int64_t T;
   int32_t tiles;              // tiles of one (row, KV head) pair
-  int32_t ctas;               // runs: each has `per` tiles, the first `more` of them one more
-  int32_t per, more;
+  int32_t ctas;               // runs: each has `per` units, the first `more` of them one more
+  int32_t unit, per, more;    // a unit is one tile, or the tiles of a pair (no run then ends inside one)
   float scale_log2;
   float* part_o;              // [2 ctas, group, 256] unnormalised outputs of pairs cut by a run's ends
   float* part_ml;             // [2 ctas, group, 2] maximum (log2 units), sum
@@ -151,7 +151,7 @@ struct Params {
 };
 
 // First tile of run i.
-__device__ __forceinline__ int run_begin(const Params& p, int i) { return i * p.per + min(i, p.more); }
+__device__ __forceinline__ int run_begin(const Params& p, int i) { return (i * p.per + min(i, p.more)) * p.unit; }
 
 // Shared-memory descriptor of an unswizzled N-major operand: cores of 8 K
 // rows of 16 bytes, k8_stride bytes from one to the next along K and
@@ -901,12 +901,12 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
   if (warp == 8) tmem_dealloc(tmem, C::TMEM);
 }
 
-// Merges the pieces of pairs cut by the end of a run: one CTA per (cut, 4
+// Merges the pieces of pairs cut by the end of a run: one CTA per (cut, 2
 // heads), two features a thread.  The CTAs of a pair's first cut merge all of its
 // pieces.  It is launched while the attention runs and waits for it.
-constexpr int MERGE_HEADS = 4, MERGE_THREADS = MERGE_HEADS * D / 2;
+constexpr int MERGE_HEADS = 2, MERGE_THREADS = MERGE_HEADS * D / 2;
 
-template <bool F16>
+template <bool F16, int BATCH>   // pieces loaded in one round trip
 __global__ void __launch_bounds__(MERGE_THREADS) combine_fp8_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -923,7 +923,6 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine_fp8_kernel(const Params
   // (plain loads: the pieces are written while this grid is already launched)
   float M = -INFINITY, sum = 0.f;
   float2 acc = make_float2(0.f, 0.f);
-  constexpr int BATCH = 8;                             // pieces loaded in one round trip
   for (int i0 = 0; i0 < pieces; i0 += BATCH) {
     float2 ml[BATCH], o[BATCH];
 #pragma unroll
