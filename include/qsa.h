@@ -446,7 +446,9 @@ size_t qsa_mqa_paged_batch_workspace_size(int32_t R, int32_t num_decodes, int32_
  *              one pool, are all strides.
  *   k_scale,   fp32 [num_pages, page_size / block_tokens, Hkv]: page and
  *   v_scale    block strides in elements, unit head stride; > 0 and finite
- *              for every block that holds a token.
+ *              for every block that holds a token.  A k_scale of 0 (memory
+ *              zeroed once) marks a block and head that holds none: attention
+ *              does not see its tokens.
  *   block_tokens  1 .. page_size, dividing page_size (any page_size >= 1).
  * The pages' K/V cache is 16-bit; this one halves its memory and traffic.
  * Requests, rows and page tables are those of qsa_sparse_attention: row i of
@@ -501,16 +503,21 @@ qsa_status_t qsa_kv_append_fp8_f16(const void* k, int64_t k_stride_t, int64_t k_
  * same definition on the keys and values that the codes and scales stand for.
  *
  * Codes enter the tensor cores as they are; queries and probabilities are
- * split into E4M3 terms (a bf16 query element exactly, a probability to 2^-12
- * relative), all sums are fp32.
+ * split into E4M3 terms (a 16-bit query element exactly, down to 2^-22 of its
+ * head's largest; a probability times its v_scale to 2^-16 relative, down to
+ * 2^-22 of the largest), all sums are fp32.
  *   weights    fp32 [T, width], row stride weights_stride (>= width), or
  *              NULL: weights[t, e] = sum over the Hq query heads of entry e's
  *              softmax probability, 0 for entries that the row does not see.
  *   workspace  16-byte aligned, qsa_sparse_attention_fp8_workspace_size(T,
  *              Hq, Hkv, width, weights != NULL) bytes; its contents do not
  *              matter before or after.
- * Other arguments, empty rows and errors as qsa_sparse_attention.  A query
- * head with a NaN or infinite element gives NaN.
+ * Other arguments, empty rows and errors as qsa_sparse_attention; besides,
+ * QSA_ERR_UNSUPPORTED when the cache spans 2^31 - 1 or more multiples of the
+ * greatest common divisor of its strides (512 GiB at a divisor of 256), or
+ * T * Hkv * ceil(width / 128) exceeds 2^30.  A query head with a NaN or infinite
+ * element gives NaN.  One launch, a second one where a row's list is cut
+ * between thread blocks, and a last one for the weights.
  */
 qsa_status_t qsa_sparse_attention_fp8(const void* q, int64_t q_stride_t, int64_t q_stride_h, int32_t Hq,
                                       const void* k_cache, const void* v_cache, const float* k_scale,

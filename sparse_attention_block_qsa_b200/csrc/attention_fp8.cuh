@@ -213,14 +213,14 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 2^-inf = 0
   return r;
 }
 
-// Arrives on bar once this thread's cp.async copies so far have landed; the
-// barrier counts this arrival like any other.
 __device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
+// Arrives on bar once this thread's cp.async copies so far have landed; the
+// barrier counts this arrival like any other.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -299,18 +299,17 @@ __device__ __forceinline__ void row_position(const int32_t* __restrict__ cu, con
 }
 
 // The entries of consecutive tiles, looked up in stages so that no load is
-// waited for: a tile's list entries two tiles and their pages one tile before
-// use.  Every lane follows the E entries from `entry` of the tile.
-template <int E>
+// waited for: a tile's list entry two tiles and its page one tile before use.
+// Every lane follows entry `entry` of the tile.
 struct Feed {
   int t, g, tile;             // row, KV head and tile of the stage that loads list entries
   int left;                   // tiles of the run it has not loaded yet
   const int32_t* pt;          // the row's page table; last token it sees
   int last;
   int entry, lane;
-  int jA[E], lastA, gA;       // list entries loaded
+  int jA, lastA, gA;          // list entry loaded
   const int32_t* ptA;
-  int jB[E], pageB[E], lastB, gB;   // pages loaded
+  int jB, pageB, lastB, gB;   // page loaded
 
   __device__ __forceinline__ void row(const Params& p) {
     int r, pos, L;
@@ -318,14 +317,16 @@ struct Feed {
     pt = p.page_table + (int64_t)r * p.pt_stride;
     last = min(pos, L - 1);
   }
-  __device__ __forceinline__ void load_entries(const Params& p) {
+  __device__ __forceinline__ int list_entry(const Params& p) {
+    const int e = tile * TILE + entry;
+    return e < p.width ? __ldg(p.tok + (int64_t)t * p.tok_stride + e) : -1;
+  }
+  // `first`: the list entry where it is loaded already
+  __device__ __forceinline__ void load_entry(const Params& p, bool loaded = false, int first = -1) {
     lastA = last;
     gA = g;
     ptA = pt;
-    const int e = tile * TILE + entry;
-    const int32_t* src = p.tok + (int64_t)t * p.tok_stride + e;
-#pragma unroll
-    for (int i = 0; i < E; ++i) jA[i] = left > 0 && e + i < p.width ? __ldg(src + i) : -1;
+    jA = loaded ? first : left > 0 ? list_entry(p) : -1;
     if (left <= 0) return;
     --left;
     if (++tile == p.tiles) {
@@ -337,17 +338,14 @@ struct Feed {
       }
     }
   }
-  __device__ __forceinline__ void load_pages(const Params& p) {
+  __device__ __forceinline__ void load_page(const Params& p) {
     gB = gA;
     lastB = lastA;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      jB[i] = jA[i];
-      pageB[i] = -1;
-      if (jB[i] >= 0) {                                // what the row may see is checked later: `last` may be in flight
-        const int lp = divide(jB[i], p.by_page);
-        if (lp < p.max_pages) pageB[i] = __ldg(ptA + lp);
-      }
+    jB = jA;
+    pageB = -1;
+    if (jB >= 0) {                                     // what the row may see is checked later: `last` may be in flight
+      const int lp = divide(jB, p.by_page);
+      if (lp < p.max_pages) pageB = __ldg(ptA + lp);
     }
   }
   __device__ __forceinline__ void start(const Params& p, int pair, int tile_, int n, int entry_, int lane_) {
@@ -357,28 +355,19 @@ struct Feed {
     t = pair / p.Hkv;
     g = pair - t * p.Hkv;
     left = n;
-    // the first tile's list entries are on their way while the row is looked up
-    int first[E];
-    const int e = tile * TILE + entry;
-#pragma unroll
-    for (int i = 0; i < E; ++i) first[i] = e + i < p.width ? __ldg(p.tok + (int64_t)t * p.tok_stride + e + i) : -1;
+    const int first = list_entry(p);                   // on its way while the row is looked up
     row(p);
-    load_entries(p);
-#pragma unroll
-    for (int i = 0; i < E; ++i) jA[i] = first[i];
-    load_pages(p);
-    load_entries(p);
+    load_entry(p, true, first);
+    load_page(p);
+    load_entry(p);
   }
-  // the next tile's entries: their pages and tokens (page < 0: not visible)
-  __device__ __forceinline__ void next(const Params& p, int (&page)[E], int (&j)[E], int& kv_head) {
+  // the next tile's entry: its page and token (page < 0: not visible)
+  __device__ __forceinline__ void next(const Params& p, int& page, int& j, int& kv_head) {
     kv_head = gB;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      j[i] = jB[i];
-      page[i] = jB[i] <= lastB && (int64_t)pageB[i] < p.num_pages ? pageB[i] : -1;
-    }
-    load_pages(p);
-    load_entries(p);
+    j = jB;
+    page = jB <= lastB && (int64_t)pageB < p.num_pages ? pageB : -1;
+    load_page(p);
+    load_entry(p);
   }
 };
 
@@ -457,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     if constexpr (C::RESIDENT > 1) regs_shrink<REGS_PROD>();
     const int w = warp - 4;
     const int u = lane & 15, row2 = lane >> 4;         // 16 lanes a row, two rows per instruction
-    Feed<1> f;
+    Feed f;
     f.start(p, pair0, tile0, n, 32 * w + lane, lane);
     // rows of the warp's 32 entries into the next buffer.  K goes one tile ahead of V: it is consumed as soon as it
     // lands, V only after the softmax.
@@ -491,11 +480,11 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     int row_v = -1;                                    // the last tile's row, whose V is still to come
     bool ok = true;
     for (int k = 0; k < n; ++k) {
-      int page[1], j[1], g;
+      int page, j, g;
       f.next(p, page, j, g);
-      const int in_page = j[0] - divide(j[0], p.by_page) * p.page_size;
-      const int row = page[0] < 0 ? -1 : page[0] * p.page_rows + in_page * p.token_rows + g * p.head_rows;
-      const int64_t at = C::RING && row >= 0 ? scale_index(p, page[0], in_page, g) : 0;
+      const int in_page = j - divide(j, p.by_page) * p.page_size;
+      const int row = page < 0 ? -1 : page * p.page_rows + in_page * p.token_rows + g * p.head_rows;
+      const int64_t at = C::RING && row >= 0 ? scale_index(p, page, in_page, g) : 0;
       ok = gather(p.k, row, k, at) && (k == 0 || gather(p.v, row_v, k - 1, -1));
       if (!ok) break;
       row_v = row;
@@ -649,7 +638,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     // ---------------------------------------------------------------- softmax
     if constexpr (C::RESIDENT > 1) regs_grow<REGS_SOFT>();
     const uint32_t tm_lane = (uint32_t)(warp * 32) << 16;
-    Feed<1> f;
+    Feed f;
     if constexpr (!C::RING) f.start(p, pair0, tile0, n, tid, lane);
     // heads 2 i, 2 i + 1: sums over this thread's entries; features tid and 128 + tid
     float2 l_run[HG / 2], o0[HG / 2], o1[HG / 2];
@@ -663,15 +652,15 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     bool fresh = true;
     // scales of the next tile's entry: loaded one tile ahead
     float ks_nx = 0.f, vs_nx = 0.f;
-    bool seen_nx = false;
     auto scales = [&]() {
-      int page[1], j[1], g;
+      int page, j, g;
       f.next(p, page, j, g);
-      seen_nx = page[0] >= 0;
-      const int in_page = j[0] - divide(j[0], p.by_page) * p.page_size;
-      const int64_t at = seen_nx ? scale_index(p, page[0], in_page, g) : 0;
-      ks_nx = __ldg(p.k_scale + at);                   // element 0 always exists; unseen entries do not use it
-      vs_nx = __ldg(p.v_scale + at);
+      ks_nx = vs_nx = 0.f;
+      if (page >= 0) {
+        const int64_t at = scale_index(p, page, j - divide(j, p.by_page) * p.page_size, g);
+        ks_nx = __ldg(p.k_scale + at);
+        vs_nx = __ldg(p.v_scale + at);
+      }
     };
     if constexpr (!C::RING) scales();
     auto output_done = [&](int k) {                // tile k's product is in TMEM, its P free
@@ -697,8 +686,8 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       }
     };
     for (int k = 0; k < n; ++k) {
-      bool seen = seen_nx;
-      float ks = ks_nx, vs = seen ? vs_nx : 0.f;
+      bool seen;
+      float ks = ks_nx, vs = vs_nx;
       float2 x[HG / 2];                                // scores, then relative to mref, then probabilities
       {
         if (!mbar_wait(&s_full[sb], sp, abort)) gone();
@@ -707,8 +696,10 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           const float* sc = sc_s + k % C::RING_TILES * 2 * TILE + tid;
           ks = sc[0];
           vs = sc[TILE];
-          seen = ks != 0.f;
         }
+        // unseen entries come with scales of 0, and a k_scale of 0 marks a block that holds nothing
+        seen = ks != 0.f;
+        if (!seen) vs = 0.f;
         if (fresh) {
 #pragma unroll
           for (int i = 0; i < HG / 2; ++i) nref[i] = l_run[i] = o0[i] = o1[i] = make_float2(0.f, 0.f);

@@ -102,10 +102,10 @@ def visible(tok_row, r, pos, seq_lens, table, pages, ps):
 def attention(q, kc, vc, ks, vs, table, cu, seq_lens, tok, scale, gate=None, half_step=2.0 ** -8):
     """out, lse, weights, and how far each may be off (see below), all float64.  q [T, Hq, 256].
 
-    Tolerances, from the arithmetic the operator promises: scores are 256 products added in fp32 (256 * 2^-24
-    of sum |q k|) of queries held to 2^-22 of the head's largest element; probabilities to 2^-12 relative and
-    2^-26 of the largest; sums and exponentials in fp32 (2^-14 relative covers width-2^10 sums); the output one
-    rounding of half_step relative."""
+    Tolerances: scores are 256 products added in fp32 (256 * 2^-24 of sum |q k|) of queries held to 2^-22 of the
+    head's largest element; probabilities at least to 2^-12 relative and, as errors of n entries of 2^-22 of the
+    largest with signs of their own, n * 2^-26 of it in all; sums and exponentials in fp32 (2^-14 relative covers
+    width-2^10 sums); the output one rounding of half_step relative.  A k_scale of 0 hides a block's tokens."""
     T, Hq, _ = q.shape
     pages, ps, H, _ = kc.shape
     bt = ps // ks.shape[1]
@@ -116,8 +116,13 @@ def attention(q, kc, vc, ks, vs, table, cu, seq_lens, tok, scale, gate=None, hal
         seen = visible(tok[t], r, pos, seq_lens, table, pages, ps)
         if not seen:
             continue
-        e, pg, rw = (np.array(c) for c in zip(*seen))
+        every = [np.array(c) for c in zip(*seen)]
         for g in range(H):
+            e, pg, rw = every
+            held = ks[pg, rw // bt, g] != 0
+            e, pg, rw = e[held], pg[held], rw[held]
+            if len(e) == 0:
+                continue
             K = VALUE[kc[pg, rw, g]] * ks[pg, rw // bt, g][:, None]
             V = VALUE[vc[pg, rw, g]] * vs[pg, rw // bt, g][:, None]
             for h in range(g * G, (g + 1) * G):
@@ -132,7 +137,7 @@ def attention(q, kc, vc, ks, vs, table, cu, seq_lens, tok, scale, gate=None, hal
                 ds = scale * float(np.max(2.0 ** -16 * (np.abs(K) @ np.abs(q[t, h])) +
                                           2.0 ** -22 * np.abs(q[t, h]).max() * np.abs(K).sum(1)))
                 t_out[t, h] = (m * ((2.0 ** -12 + 2.0 ** -14 + 4 * ds) * (p @ np.abs(V)) +
-                                    len(seen) * 2.0 ** -26 * np.abs(V).max()) +
+                                    len(e) * 2.0 ** -26 * np.abs(V).max()) +
                                half_step * np.abs(out[t, h]) + 1e-6)
                 t_lse[t, h] = 2 * ds + 4e-6 * (abs(lse[t, h]) + 1)
                 np.add.at(t_w[t], e, p * (4 * ds + 8e-6 * (abs(lse[t, h]) + 1)) + 1e-12)

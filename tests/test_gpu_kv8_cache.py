@@ -136,6 +136,43 @@ def test_append_layouts():
     assert torch.all(sc[:, :, :, 2:] == 0)
 
 
+def test_append_behind_4_gib_and_on_another_stream():
+    d = append_inputs([70, 40], [20, 3], 2, 64, 16, seed=19)
+    want = gpu_append(d)
+    pages, n = 140000, d["kc"].shape[0]
+    pools = {k: torch.zeros((pages, *d[k].shape[1:]), dtype=d[k].dtype, device=DEV) for k in ("kc", "vc", "ks", "vs")}
+    assert pools["kc"].numel() > 1 << 32
+    at = torch.arange(n) + pages - n
+    for k in pools:
+        pools[k][at.to(DEV)] = d[k].to(DEV)
+    table = torch.where(d["table"] >= 0, d["table"] + (pages - n), d["table"])
+    x = [d[k].to(DEV) for k in "kv"]
+    rest = [table.to(DEV), d["cu"].to(DEV), d["sl"].to(DEV)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    qsa.kv_append_fp8(*x, *pools.values(), *rest, stream=side)
+    torch.cuda.synchronize()
+    for k in pools:
+        assert torch.equal(pools[k][pages - n:].cpu(), want[k])
+        assert not torch.any(pools[k][:1000].view(torch.uint8))
+
+
+def test_append_captured_into_a_graph():
+    d = append_inputs([70, 5, 200], [4, 3, 2], 2, 64, 16, seed=9)
+    want = gpu_append(d)
+    c = {n: d[n].clone().to(DEV) for n in ("kc", "vc", "ks", "vs")}
+    args = [d["k"].to(DEV), d["v"].to(DEV), *c.values(), d["table"].to(DEV), d["cu"].to(DEV), d["sl"].to(DEV)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qsa.kv_append_fp8(*args)
+    for n in c:
+        c[n].copy_(d[n])
+    g.replay()
+    g.replay()                                       # the same rows again: nothing more to grow
+    torch.cuda.synchronize()
+    assert all(torch.equal(c[n].cpu(), want[n]) for n in c)
+
+
 # ------------------------------------------------------------------ accumulate
 
 @pytest.mark.parametrize("ps,width", [(16, 1), (64, 130), (196, 700), (1, 33)])
@@ -233,6 +270,25 @@ def test_evict_large_and_negative_weights_and_strides():
     assert out is t
     assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip((out, freed, counts), want))
     assert torch.all(wide[:2, :, width:] == -5)
+
+
+def test_evict_captured_in_place():
+    table, sl, cu, pages = ref.layout([5000, 160], [1, 1], 16, 2)
+    tw = torch.randint(0, 1 << 40, (pages, 16), generator=torch.Generator().manual_seed(4))
+    keep = torch.tensor([100, 4], dtype=torch.int32)
+    want = ref.evict(tw.numpy(), table.numpy(), sl.numpy(), keep.numpy(), 1, 1)
+    t, args = table.to(DEV), (tw.to(DEV), sl.to(DEV), keep.to(DEV))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _, freed, counts = qsa.evict_pages(args[0], t, args[1], args[2], 1, 1, table_out=t)
+    for _ in range(2):
+        t.copy_(table)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip((t, freed, counts), want))
+    g.replay()                                       # the pages are gone already
+    torch.cuda.synchronize()
+    assert counts.tolist() == [0, 0] and torch.all(freed == -1) and np.array_equal(t.cpu().numpy(), want[0])
 
 
 def test_evict_empty():
