@@ -153,6 +153,19 @@ struct Params {
 // First tile of run i.
 __device__ __forceinline__ int run_begin(const Params& p, int i) { return (i * p.per + min(i, p.more)) * p.unit; }
 
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Shared-memory descriptor of an unswizzled N-major operand: cores of 8 K
 // rows of 16 bytes, k8_stride bytes from one to the next along K and
 // mn16_stride along N.  (The swizzled M-major operand, 128 bytes of M per K
