@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     // ---------------------------------------------------------------- gather
     if constexpr (C::RESIDENT > 1) regs_shrink<REGS_PROD>();
     const int w = warp - 4;
-    const int u = lane & 15, row2 = lane >> 4;         // 16 lanes a row, two rows per instruction
+    const int u = lane & 7, row4 = lane >> 3;          // 8 lanes a row (16 bytes of each half), 4 rows an instruction
     Feed f;
     f.start(p, pair0, tile0, n, 32 * w + lane, lane);
     // rows of the warp's 32 entries into the next buffer.  K goes one tile ahead of V: it is consumed as soon as it
@@ -467,24 +467,28 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     auto gather = [&](const uint8_t* base, int row, int tile, int64_t scale_at) -> bool {
       const int b = item % BUFS;
       if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[b], (uint32_t)((item / BUFS) & 1) ^ 1, abort))) return false;
-      const uint32_t dst = smem_addr(buf_s + b * BUF_BYTES) + (u >> 3) * HALF_BYTES + (32 * w + row2) * 128;
+      const uint32_t dst = smem_addr(buf_s + b * BUF_BYTES) + (32 * w + row4) * 128;
       const uint8_t* src = base + u * 16;
       if (C::RING && scale_at >= 0) {                  // the tile's scales land with its K rows
         const uint32_t at = smem_addr(sc_s + tile % C::RING_TILES * 2 * TILE + 32 * w + lane);
         cp_async4(at, p.k_scale + scale_at, row >= 0);
         cp_async4(at + TILE * 4, p.v_scale + scale_at, row >= 0);
       }
-      int rr[16];                                      // all the look-ups before the copies
+      int rr[8];                                       // all the look-ups before the copies
 #pragma unroll
-      for (int i = 0; i < 16; ++i) rr[i] = __shfl_sync(0xffffffffu, row, 2 * i + row2);
-      auto place = [&](int i) { return dst + i * 256 + (((u & 7) ^ ((2 * i + row2) & 7)) << 4); };
-      if (__all_sync(0xffffffffu, row >= 0)) {
+      for (int i = 0; i < 8; ++i) rr[i] = __shfl_sync(0xffffffffu, row, 4 * i + row4);
+      const bool full = __all_sync(0xffffffffu, row >= 0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) cp_async16_all(place(i), src + (uint64_t)(uint32_t)rr[i] * p.pitch);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          attn::cp_async16(place(i), src + (uint64_t)(uint32_t)max(rr[i], 0) * p.pitch, rr[i] >= 0);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t to = dst + i * 512 + ((u ^ (4 * (i & 1) + row4)) << 4);
+        const uint8_t* from = src + (uint64_t)(uint32_t)max(rr[i], 0) * p.pitch;
+        if (full) {
+          cp_async16_all(to, from);
+          cp_async16_all(to + HALF_BYTES, from + 128);
+        } else {
+          attn::cp_async16(to, from, rr[i] >= 0);
+          attn::cp_async16(to + HALF_BYTES, from + 128, rr[i] >= 0);
+        }
       }
       cp_async_arrive(&kv_full[b]);
       ++item;
