@@ -588,8 +588,10 @@ qsa_status_t qsa_accumulate_weights(const float* weights, int64_t weights_stride
  * cache of page_size / 4 rows per page can share the table.  A page that
  * several requests share is dropped for each on its own: the caller counts
  * references.  keep, seq_lens: int32 [R].
- *   workspace  16-byte aligned, qsa_evict_pages_workspace_size(R, max_pages)
- *              bytes.
+ *   workspace  16-byte aligned, qsa_evict_pages_workspace_size(R, max_pages,
+ *              page_size) bytes; 0 (NULL will do) for few requests with short
+ *              tables (32,768 tokens).
+ * One launch without a workspace, two with one.
  */
 qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int32_t page_size,
                              const int32_t* page_table, int64_t pt_stride, int32_t max_pages, const int32_t* seq_lens,
@@ -597,7 +599,7 @@ qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int
                              int64_t out_stride, int32_t* freed, int64_t freed_stride, int32_t* counts,
                              void* workspace, size_t workspace_bytes, void* stream);
 
-size_t qsa_evict_pages_workspace_size(int32_t R, int32_t max_pages);
+size_t qsa_evict_pages_workspace_size(int32_t R, int32_t max_pages, int32_t page_size);
 
 #ifdef __cplusplus
 }

@@ -65,7 +65,7 @@ SIGNATURES = {
                                          _i64, _i32, _vp]),
     "qsa_evict_pages": (C.c_int, [_vp, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i64, _vp,
                                   _i64, _vp, _vp, _sz, _vp]),
-    "qsa_evict_pages_workspace_size": (_sz, [_i32, _i32]),
+    "qsa_evict_pages_workspace_size": (_sz, [_i32, _i32, _i32]),
 }
 
 STATUS = {0: "QSA_OK", 1: "QSA_ERR_INVALID_ARG", 2: "QSA_ERR_ALIGNMENT", 3: "QSA_ERR_UNSUPPORTED",
@@ -679,8 +679,8 @@ def accumulate_weights(weights: torch.Tensor, token_idx: torch.Tensor, page_tabl
     return token_weight
 
 
-def evict_pages_workspace_size(R: int, max_pages: int) -> int:
-    return int(lib().qsa_evict_pages_workspace_size(R, max_pages))
+def evict_pages_workspace_size(R: int, max_pages: int, page_size: int) -> int:
+    return int(lib().qsa_evict_pages_workspace_size(R, max_pages, page_size))
 
 
 def evict_pages(token_weight: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, keep: torch.Tensor,
@@ -722,7 +722,7 @@ def evict_pages(token_weight: torch.Tensor, page_table: torch.Tensor, seq_lens: 
         _want(counts, "counts", torch.int32, 1, dev)
         if counts.shape[0] != R or not counts.is_contiguous():
             raise ValueError("counts must be contiguous int32 [R]")
-    wp, nbytes, workspace = _workspace(workspace, evict_pages_workspace_size(R, max_pages) if workspace is None else 0,
+    wp, nbytes, workspace = _workspace(workspace, evict_pages_workspace_size(R, max_pages, ps) if workspace is None else 0,
                                        stream, dev)
     _call(dev, "qsa_evict_pages", token_weight.data_ptr(), pages, ps, page_table.data_ptr(), pts[0], max_pages,
           seq_lens.data_ptr(), keep.data_ptr(), R, keep_first, keep_last, table_out.data_ptr(), out0,

@@ -12,10 +12,11 @@
 //    counted in units of 2^-32 in 64-bit integers: the order of the atomics
 //    cannot change the sums.  4.2 M entries take 13.6 us, whatever a warp holds:
 //    the rate of 64-bit atomics (310 G/s).
-//  * page_weight_kernel, evict_kernel: groups of lanes sum the tokens of a
-//    logical page each; one CTA per request finds the lightest pages by a radix
-//    selection over the 64-bit sums and writes the new table and the freed
-//    pages in order.
+//  * evict_kernel: one CTA per request.  Groups of lanes sum the tokens of a
+//    logical page each, then the CTA finds the lightest pages by a radix
+//    selection over the 64-bit sums and writes the new table and the freed pages
+//    in order.  For long tables, which one SM would read too slowly, and many
+//    requests page_weight_kernel sums the pages on the whole GPU first.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -263,15 +264,63 @@ struct EvictParams {
   unsigned long long* key;      // workspace [R, max_pages]: page weight, ordered as an unsigned number
 };
 
+// Token weights of WEIGH_EACH pages at a time, `lanes` lanes a page, two tokens a
+// load where rows allow it.  Pages below 0 have none.  The sums over lanes are
+// scattered on the way (each step halves what a lane holds, 18 shuffles instead
+// of 80 at 32 lanes): put(b, sum) is called once for every page.
+constexpr int WEIGH_EACH = 8;
+
+template <bool PAIRS, typename Put>
+__device__ __forceinline__ void weigh(const EvictParams& p, const int (&page)[WEIGH_EACH], int sub, int lanes, Put put) {
+  unsigned long long v[WEIGH_EACH];
+#pragma unroll
+  for (int b = 0; b < WEIGH_EACH; ++b) v[b] = 0;
+  constexpr int STEP = PAIRS ? 2 : 1;
+  for (int e = STEP * sub; e < p.page_size; e += STEP * lanes) {
+#pragma unroll
+    for (int b = 0; b < WEIGH_EACH; ++b) {
+      if (page[b] < 0) continue;
+      const int64_t* w = p.token_weight + (int64_t)page[b] * p.page_size + e;
+      if (PAIRS) {
+        const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2*>(w));
+        v[b] += x.x + x.y;
+      } else {
+        v[b] += __ldg(reinterpret_cast<const unsigned long long*>(w));
+      }
+    }
+  }
+  int first = 0, held = WEIGH_EACH, o = lanes >> 1;    // this lane holds pages first .. first + held - 1
+#pragma unroll
+  for (int half = WEIGH_EACH / 2; half >= 1; half >>= 1) {
+    if (o > 0) {
+      const bool upper = (sub & o) != 0;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const unsigned long long keep = upper ? v[i + half] : v[i], give = upper ? v[i] : v[i + half];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+      first += upper ? half : 0;
+      held = half;
+      o >>= 1;
+    }
+  }
+  const int copies = o > 0 ? 2 * o : 1;                // lanes that end with the same page
+  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  if ((sub & (copies - 1)) == 0) {
+#pragma unroll
+    for (int i = 0; i < WEIGH_EACH; ++i)
+      if (i < held) put(first + i, v[i]);
+  }
+}
+
 __device__ __forceinline__ int logical_pages(const EvictParams& p, int r) {
   const int L = __ldg(p.seq_lens + r);
   return L <= 0 ? 0 : (int)min((int64_t)p.max_pages, ((int64_t)L + p.page_size - 1) / p.page_size);
 }
 
-// Page weights: `lanes` lanes (a power of two) sum a page, two tokens a load
-// where rows allow it; every group of lanes takes WEIGH_EACH logical pages of one
-// request, all in flight at once.
-constexpr int WEIGH_THREADS = 128, WEIGH_EACH = 8;
+// Page weights into the workspace: every group of lanes takes WEIGH_EACH
+// logical pages of one request, all in flight at once.
+constexpr int WEIGH_THREADS = 128;
 
 template <bool PAIRS>
 __global__ void __launch_bounds__(WEIGH_THREADS) page_weight_kernel(const EvictParams p, int lanes) {
@@ -285,43 +334,24 @@ __global__ void __launch_bounds__(WEIGH_THREADS) page_weight_kernel(const EvictP
     page_s[i] = page < p.num_pages ? page : -1;
   }
   __syncthreads();
-  unsigned long long sum[WEIGH_EACH];
-  const int64_t* w[WEIGH_EACH];
+  int page[WEIGH_EACH];
 #pragma unroll
-  for (int b = 0; b < WEIGH_EACH; ++b) {
-    const int page = page_s[b * groups + group];
-    sum[b] = 0;
-    w[b] = page < 0 ? nullptr : p.token_weight + (int64_t)page * p.page_size;
-  }
-  constexpr int STEP = PAIRS ? 2 : 1;
-  for (int e = STEP * sub; e < p.page_size; e += STEP * lanes) {
-#pragma unroll
-    for (int b = 0; b < WEIGH_EACH; ++b) {
-      if (!w[b]) continue;
-      if (PAIRS) {
-        const ulonglong2 v = __ldg(reinterpret_cast<const ulonglong2*>(w[b] + e));
-        sum[b] += v.x + v.y;
-      } else {
-        sum[b] += __ldg(reinterpret_cast<const unsigned long long*>(w[b] + e));
-      }
-    }
-  }
+  for (int b = 0; b < WEIGH_EACH; ++b) page[b] = page_s[b * groups + group];
   unsigned long long* key = p.key + (int64_t)r * p.max_pages + base;
-#pragma unroll
-  for (int b = 0; b < WEIGH_EACH; ++b) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], o);
-    if (sub == 0 && w[b]) key[b * groups + group] = sum[b] ^ (1ull << 63);
-  }
+  weigh<PAIRS>(p, page, sub, lanes, [&](int b, unsigned long long sum) {
+    if (page_s[b * groups + group] >= 0) key[b * groups + group] = sum ^ (1ull << 63);
+  });
 }
 
-// Selection: one CTA per request; a thread holds PER consecutive pages in
-// registers (PER * EVICT_THREADS >= max_pages) or, for longer tables (PER = 0),
-// looks them up again in every pass.
-constexpr int EVICT_THREADS = 512;
+// Selection: a thread holds PER consecutive pages in registers (PER * THREADS
+// >= max_pages) or, for longer tables (PER = 0), looks them up again in every
+// pass.
 constexpr int BINS = 512;                              // of a pass: 9 bits
 constexpr int PASSES = 8;                              // the first and up to 61 open bits after it
+enum Weights { FROM_WORKSPACE, HERE, HERE_IN_PAIRS };  // where the page weights come from
 
 // Exclusive prefix over the CTA of one int per thread, and the total.
+template <int THREADS>
 __device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int inc = v;
@@ -333,7 +363,7 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
   __syncthreads();                                     // warp_s may still be read
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
-  constexpr int WARPS = EVICT_THREADS / 32;
+  constexpr int WARPS = THREADS / 32;
   int ws = lane < WARPS ? warp_s[lane] : 0, wi = ws;   // every warp scans the warp sums
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -344,9 +374,10 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
   return __shfl_sync(0xffffffffu, wi - ws, warp) + inc - v;
 }
 
-template <int PER>
-__global__ void __launch_bounds__(EVICT_THREADS) evict_kernel(const EvictParams p) {
-  __shared__ int warp_s[EVICT_THREADS / 32];
+template <int THREADS, int PER, Weights FORM>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_kernel(const EvictParams p, int lanes) {
+  extern __shared__ unsigned long long key_s[];        // page weights summed here
+  __shared__ int warp_s[THREADS / 32];
   __shared__ int hist_s[PASSES][BINS];
   __shared__ unsigned long long and_s, or_s;
   __shared__ int held_s, free_s, bin_s, left_s;
@@ -355,7 +386,7 @@ __global__ void __launch_bounds__(EVICT_THREADS) evict_kernel(const EvictParams 
   const int32_t* row = p.page_table + (int64_t)r * p.pt_stride;
   int32_t* out = p.table_out + (int64_t)r * p.out_stride;
   int32_t* freed = p.freed + (int64_t)r * p.freed_stride;
-  const unsigned long long* keys = p.key + (int64_t)r * p.max_pages;
+  const unsigned long long* keys = FORM == FROM_WORKSPACE ? p.key + (int64_t)r * p.max_pages : key_s;
   const int want_keep = __ldg(p.keep + r);
   auto is_live = [&](int lp, int entry) { return lp < n && entry >= 0 && entry < p.num_pages; };
   auto is_held = [&](int lp) { return lp < p.keep_first || lp >= n - p.keep_last; };
@@ -376,18 +407,33 @@ __global__ void __launch_bounds__(EVICT_THREADS) evict_kernel(const EvictParams 
       n_free += may[i];
     }
   } else {
-    for (int lp = tid; lp < n; lp += EVICT_THREADS)
+    for (int lp = tid; lp < n; lp += THREADS)
       if (is_live(lp, row[lp])) (is_held(lp) ? n_held : n_free)++;
   }
+  for (int i = tid; i < PASSES * BINS; i += THREADS) hist_s[i / BINS][i % BINS] = 0;
+  if (FORM != FROM_WORKSPACE) {
+    int* page_s = reinterpret_cast<int*>(key_s + HOLD * THREADS);
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) hist_s[i][tid] = 0;
+    for (int i = 0; i < HOLD; ++i) page_s[tid * HOLD + i] = may[i] ? entry[i] : -1;
+    __syncthreads();
+    const int sub = tid & (lanes - 1), group = tid / lanes, groups = THREADS / lanes;
+    for (int base = 0; base < n; base += groups * WEIGH_EACH) {
+      auto at = [&](int b) { return base + b * groups + group; };
+      int page[WEIGH_EACH];
+#pragma unroll
+      for (int b = 0; b < WEIGH_EACH; ++b) page[b] = at(b) < n ? page_s[at(b)] : -1;
+      weigh<FORM == HERE_IN_PAIRS>(p, page, sub, lanes, [&](int b, unsigned long long sum) {
+        if (at(b) < n) key_s[at(b)] = sum ^ (1ull << 63);
+      });
+    }
+  }
   if (tid == 0) {
     and_s = ~0ull;
     or_s = 0;
     held_s = free_s = 0;
   }
   __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the page weights
+  if (FORM == FROM_WORKSPACE) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (PER > 0) {
 #pragma unroll
     for (int i = 0; i < HOLD; ++i) key[i] = may[i] ? keys[tid * HOLD + i] : 0;
@@ -399,7 +445,7 @@ __global__ void __launch_bounds__(EVICT_THREADS) evict_kernel(const EvictParams 
       for (int i = 0; i < HOLD; ++i)
         if (may[i]) f(key[i]);
     } else {
-      for (int lp = tid; lp < n; lp += EVICT_THREADS)
+      for (int lp = tid; lp < n; lp += THREADS)
         if (is_live(lp, row[lp]) && !is_held(lp)) f(keys[lp]);
     }
   };
@@ -497,7 +543,7 @@ __global__ void __launch_bounds__(EVICT_THREADS) evict_kernel(const EvictParams 
       int ties = 0;
 #pragma unroll
       for (int i = 0; i < HOLD; ++i) ties += may[i] && (key[i] & mask) == prefix;
-      rank = block_prefix(ties, warp_s, total);
+      rank = block_prefix<THREADS>(ties, warp_s, total);
     }
     bool stays[HOLD];
     int gone = 0;
@@ -509,7 +555,7 @@ __global__ void __launch_bounds__(EVICT_THREADS) evict_kernel(const EvictParams 
       rank += tie;
       gone += !stays[i];
     }
-    int at = block_prefix(gone, warp_s, total);
+    int at = block_prefix<THREADS>(gone, warp_s, total);
 #pragma unroll
     for (int i = 0; i < HOLD; ++i) {
       const int lp = tid * HOLD + i;
@@ -517,28 +563,28 @@ __global__ void __launch_bounds__(EVICT_THREADS) evict_kernel(const EvictParams 
       out[lp] = stays[i] ? entry[i] : -1;
       if (!stays[i]) freed[at++] = entry[i];
     }
-    for (int i = total + tid; i < p.max_pages; i += EVICT_THREADS) freed[i] = -1;
+    for (int i = total + tid; i < p.max_pages; i += THREADS) freed[i] = -1;
     if (tid == 0) p.counts[r] = total;
   } else {
     int ties = 0, gone = 0;
-    for (int base = 0; base < p.max_pages; base += EVICT_THREADS) {
+    for (int base = 0; base < p.max_pages; base += THREADS) {
       const int lp = base + tid;
       const int e = lp < p.max_pages ? row[lp] : -1;
       const bool drop = is_live(lp, e) && !is_held(lp);
       const unsigned long long k = drop ? keys[lp] & mask : 0;
       const bool tie = some && drop && k == prefix;
       int total;
-      const int rank = ties + block_prefix(tie ? 1 : 0, warp_s, total);
+      const int rank = ties + block_prefix<THREADS>(tie ? 1 : 0, warp_s, total);
       ties += total;
       const bool stays = !drop || quota >= all_free || (some && (k > prefix || (tie && rank < want)));
-      const int to = gone + block_prefix(stays ? 0 : 1, warp_s, total);
+      const int to = gone + block_prefix<THREADS>(stays ? 0 : 1, warp_s, total);
       gone += total;
       if (lp < p.max_pages) {
         out[lp] = stays ? e : -1;
         if (!stays) freed[to] = e;
       }
     }
-    for (int i = gone + tid; i < p.max_pages; i += EVICT_THREADS) freed[i] = -1;
+    for (int i = gone + tid; i < p.max_pages; i += THREADS) freed[i] = -1;
     if (tid == 0) p.counts[r] = gone;
   }
 }

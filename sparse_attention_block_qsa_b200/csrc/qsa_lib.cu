@@ -152,6 +152,8 @@ qsa_status_t device_info(int* sms) {
         {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>), qsa::attn8::Cfg<true, 8>::SMEM},
         {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>), qsa::attn8::Cfg<true, 12>::SMEM},
         {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 16>), qsa::attn8::Cfg<true, 16>::SMEM},
+        {reinterpret_cast<const void*>(qsa::kv8::evict_kernel<1024, 4, qsa::kv8::HERE>), 4096 * 12},
+        {reinterpret_cast<const void*>(qsa::kv8::evict_kernel<1024, 4, qsa::kv8::HERE_IN_PAIRS>), 4096 * 12},
         {reinterpret_cast<const void*>(qsa::topk::topk_rows_kernel), qsa::topk::ROWS_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_pipe_kernel), qsa::topk::PIPE_SMEM_BYTES},
         {reinterpret_cast<const void*>(qsa::topk::topk_filter_kernel), qsa::topk::TP_SMEM_BYTES},
@@ -1496,10 +1498,27 @@ qsa_status_t qsa_accumulate_weights(const float* weights, int64_t weights_stride
   return launch_status("weight accumulation kernel");
 }
 
-size_t qsa_evict_pages_workspace_size(int32_t R, int32_t max_pages) {
-  if (R <= 0 || max_pages <= 0) return 0;
+// Whether one CTA per request sums its pages itself, in one launch: a CTA reads about 50 GB/s, so for tables of 32,768
+// tokens (256 KB) that is 5 us, less than a second launch costs the host.  16 requests of 102,400 tokens take 22.7 us
+// this way and 8.7 us with two launches; with more requests than SMs the CTAs queue (256 of 40,000: 22.5 and 18).
+static bool evict_in_one(int32_t R, int32_t max_pages, int32_t page_size) {
+  return R <= 148 && max_pages <= 4096 && (int64_t)max_pages * page_size <= 32768;
+}
+
+size_t qsa_evict_pages_workspace_size(int32_t R, int32_t max_pages, int32_t page_size) {
+  if (R <= 0 || max_pages <= 0 || page_size <= 0 || evict_in_one(R, max_pages, page_size)) return 0;
   return (size_t)R * (size_t)max_pages * sizeof(uint64_t);
 }
+
+extern "C++" {
+template <int THREADS, int PER>
+static void launch_evict(const qsa::kv8::EvictParams& p, int lanes, bool pairs, cudaStream_t s) {
+  using namespace qsa::kv8;
+  const size_t smem = (size_t)THREADS * PER * 12;       // a weight and an entry a page
+  if (pairs) evict_kernel<THREADS, PER, HERE_IN_PAIRS><<<(unsigned)p.R, THREADS, smem, s>>>(p, lanes);
+  else evict_kernel<THREADS, PER, HERE><<<(unsigned)p.R, THREADS, smem, s>>>(p, lanes);
+}
+}  // extern "C++"
 
 qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int32_t page_size,
                              const int32_t* page_table, int64_t pt_stride, int32_t max_pages, const int32_t* seq_lens,
@@ -1517,7 +1536,7 @@ qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int
     return fail(QSA_ERR_ALIGNMENT, "token_weight must be 8-byte, the index arrays 4-byte aligned");
   if (max_pages > 0 && R > 1 && (pt_stride < max_pages || out_stride < max_pages || freed_stride < max_pages))
     return fail(QSA_ERR_INVALID_ARG, "pt_stride, out_stride and freed_stride must be >= max_pages");
-  const size_t need = qsa_evict_pages_workspace_size(R, max_pages);
+  const size_t need = qsa_evict_pages_workspace_size(R, max_pages, page_size);
   if (max_pages > 0) {
     const Range rin = span(page_table, 4, R, R > 1 ? pt_stride : 0, 1, 0, 1, 0, max_pages);
     const Range rout = span(table_out, 4, R, R > 1 ? out_stride : 0, 1, 0, 1, 0, max_pages);
@@ -1525,9 +1544,9 @@ qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int
     const bool in_place = table_out == page_table && (R == 1 || out_stride == pt_stride);
     if ((!in_place && overlaps(rin, rout)) || overlaps(rf, rin) || overlaps(rf, rout))
       return fail(QSA_ERR_INVALID_ARG, "table_out must be page_table itself or apart from it, and freed apart from both");
-    if (!workspace || workspace_bytes < need)
+    if (need > 0 && (!workspace || workspace_bytes < need))
       return fail(QSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace_bytes, need);
-    if (!aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+    if (need > 0 && !aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   }
   int sms = 0;
   st = device_info(&sms);
@@ -1570,17 +1589,18 @@ qsa_status_t qsa_evict_pages(const int64_t* token_weight, int64_t num_pages, int
       q.key += (int64_t)r0 * max_pages;
     }
     q.counts += r0;
-    const dim3 grid(spans, (unsigned)rows);
-    if (spans > 0) {
-      if (pairs) qsa::kv8::page_weight_kernel<true><<<grid, qsa::kv8::WEIGH_THREADS, 0, s>>>(q, lanes);
-      else qsa::kv8::page_weight_kernel<false><<<grid, qsa::kv8::WEIGH_THREADS, 0, s>>>(q, lanes);
+    using namespace qsa::kv8;
+    if (need == 0) {
+      if (max_pages <= 1024) launch_evict<1024, 1>(q, lanes, pairs, s);
+      else launch_evict<1024, 4>(q, lanes, pairs, s);
+      continue;
     }
-    const dim3 one((unsigned)rows), threads(qsa::kv8::EVICT_THREADS);
-    if (max_pages <= qsa::kv8::EVICT_THREADS) launch_pdl(qsa::kv8::evict_kernel<1>, one, threads, 0, s, q);
-    else if (max_pages <= 2 * qsa::kv8::EVICT_THREADS) launch_pdl(qsa::kv8::evict_kernel<2>, one, threads, 0, s, q);
-    else if (max_pages <= 4 * qsa::kv8::EVICT_THREADS) launch_pdl(qsa::kv8::evict_kernel<4>, one, threads, 0, s, q);
-    else if (max_pages <= 8 * qsa::kv8::EVICT_THREADS) launch_pdl(qsa::kv8::evict_kernel<8>, one, threads, 0, s, q);
-    else launch_pdl(qsa::kv8::evict_kernel<0>, one, threads, 0, s, q);
+    const dim3 grid(spans, (unsigned)rows);
+    if (pairs) page_weight_kernel<true><<<grid, WEIGH_THREADS, 0, s>>>(q, lanes);
+    else page_weight_kernel<false><<<grid, WEIGH_THREADS, 0, s>>>(q, lanes);
+    const dim3 one((unsigned)rows), threads(512);
+    if (max_pages <= 4096) launch_pdl(evict_kernel<512, 8, FROM_WORKSPACE>, one, threads, 0, s, q, lanes);
+    else launch_pdl(evict_kernel<512, 0, FROM_WORKSPACE>, one, threads, 0, s, q, lanes);
   }
   return launch_status("page eviction kernels");
 }

@@ -263,13 +263,27 @@ def test_evict_large_and_negative_weights_and_strides():
     wide = torch.full((3, R, width + 9), -5, dtype=torch.int32, device=DEV)
     wide[0, :, :width] = table.to(DEV)
     t = wide[0, :, :width]
-    ws = torch.empty(qsa.evict_pages_workspace_size(R, width), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(qsa.evict_pages_workspace_size(R, width, 8), dtype=torch.uint8, device=DEV)
     out, freed, counts = qsa.evict_pages(tw.to(DEV), t, sl.to(DEV), keep.to(DEV), 1, 2, table_out=t,
                                          freed=wide[1, :, :width], workspace=ws)
     torch.cuda.synchronize()
     assert out is t
     assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip((out, freed, counts), want))
     assert torch.all(wide[:2, :, width:] == -5)
+
+
+@pytest.mark.parametrize("R,tokens,ps", [(2, 4000, 4), (3, 210000, 64), (150, 700, 1), (150, 9000, 4), (1, 90000, 16)])
+def test_evict_forms(R, tokens, ps):
+    """Tables of up to 1,024, 4,096 and more pages, few and many requests, short and long."""
+    seq_lens = [max(1, tokens - 137 * i * tokens // 30000) for i in range(R)]
+    table, sl, cu, pages = ref.layout(seq_lens, [1] * R, ps, R)
+    g = torch.Generator().manual_seed(R)
+    tw = torch.randint(0, 1 << 20, (pages, ps), generator=g) << torch.randint(0, 20, (pages, 1), generator=g)
+    tw[: pages // 3] = 5                             # many equal pages
+    keep = torch.tensor([-(-n // ps) * (1 + i % 5) // 6 for i, n in enumerate(seq_lens)], dtype=torch.int32)
+    want = ref.evict(tw.numpy(), table.numpy(), sl.numpy(), keep.numpy(), 1, 1)
+    got = gpu_evict(tw, table, sl, keep, 1, 1)
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))
 
 
 def test_evict_captured_in_place():

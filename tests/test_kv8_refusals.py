@@ -99,13 +99,17 @@ def test_accumulate_refuses(kw, code):
     assert st == code and detail, (st, detail)
 
 
+LONG = dict(maxp=5000, pts=5000, ost=5000, fst=5000)   # a table that needs a workspace
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(tw=0), INVALID), (dict(keep=0), INVALID), (dict(counts=0), INVALID), (dict(out=0), INVALID),
     (dict(freed=0), INVALID), (dict(tw=A + 4), ALIGN), (dict(keep=A + 3 * S + 1), ALIGN), (dict(first=-1), INVALID),
     (dict(last=-1), INVALID), (dict(R=-1), INVALID), (dict(maxp=-1), INVALID), (dict(pts=9), INVALID),
     (dict(ost=9), INVALID), (dict(fst=9), INVALID), (dict(out=A + S + 4), INVALID), (dict(out=A + S, ost=11), INVALID),
-    (dict(freed=A + S), INVALID), (dict(freed=A + 4 * S + 40), INVALID), (dict(ws=0), WS), (dict(nbytes=100), WS),
-    (dict(ws=A + 7 * S + 8), ALIGN), (dict(ps=0), INVALID), (dict(pages=0), INVALID),
+    (dict(freed=A + S), INVALID), (dict(freed=A + 4 * S + 40), INVALID), (dict(LONG, ws=0), WS),
+    (dict(LONG, nbytes=5000 * 32 - 1), WS), (dict(LONG, ws=A + 7 * S + 8), ALIGN), (dict(ps=0), INVALID),
+    (dict(pages=0), INVALID),
 ])
 def test_evict_refuses(kw, code):
     st, detail = evict(**kw)
@@ -121,7 +125,10 @@ def test_workspace_sizes():
     size = L.qsa_sparse_attention_fp8_workspace_size
     assert size(0, 24, 2, 67, 0) == size(8, 23, 2, 67, 0) == size(8, 24, 2, 0, 1) == 0
     assert size(8, 24, 2, 67, 1) >= size(8, 24, 2, 67, 0) > 0
-    assert L.qsa_evict_pages_workspace_size(4, 10) >= 320 and L.qsa_evict_pages_workspace_size(0, 10) == 0
+    evict_size = L.qsa_evict_pages_workspace_size
+    assert evict_size(4, 512, 64) == evict_size(148, 4096, 8) == evict_size(0, 5000, 16) == 0
+    assert evict_size(4, 513, 64) >= 4 * 513 * 8 and evict_size(1, 4097, 1) >= 4097 * 8
+    assert evict_size(149, 10, 1) >= 149 * 80
 
 
 def test_binding_refuses_tensors_that_are_not_on_a_gpu():
