@@ -8,6 +8,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 
@@ -470,14 +471,13 @@ def _raw_stream(stream, dev):
 def _new(stream, shape, dtype, dev):
     """Memory that belongs to the stream the call runs on (an output or a workspace made here)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_raw_stream(stream, dev), device=_DEVICES[dev])
+        stream = torch.cuda.ExternalStream(_raw_stream(stream, dev), device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-_DEVICES = [torch.device("cuda", i) for i in range(64)]
 _entries: dict = {}
 
 
@@ -500,7 +500,7 @@ def _workspace(workspace, need, stream, dev):
     if workspace is None:
         if need <= 0:
             return 0, 0, None
-        workspace = _new(stream, (need,), torch.uint8, dev)
+        workspace = _new(stream, need, torch.uint8, dev)
         return workspace.data_ptr(), need, workspace
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
@@ -592,6 +592,7 @@ def kv_append_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
           _raw_stream(stream, dev))
 
 
+@functools.lru_cache(maxsize=1024)
 def sparse_attention_fp8_workspace_size(T: int, Hq: int, Hkv: int, width: int, weights: bool = False) -> int:
     return int(lib().qsa_sparse_attention_fp8_workspace_size(T, Hq, Hkv, width, 1 if weights else 0))
 
@@ -648,8 +649,7 @@ def sparse_attention_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
             raise ValueError("lse must be contiguous fp32 [T, Hq]")
     need = 0
     if workspace is None:
-        need = lib().qsa_sparse_attention_fp8_workspace_size(T, Hq, Hkv, width if width > 0 else 1,
-                                                             0 if weights is None else 1)
+        need = sparse_attention_fp8_workspace_size(T, Hq, Hkv, width if width > 0 else 1, weights is not None)
     wp, nbytes, workspace = _workspace(workspace, need, stream, dev)
     _call(dev, "qsa_sparse_attention_fp8_f16" if dt == torch.float16 else "qsa_sparse_attention_fp8",
           q.data_ptr(), qs[0], qs[1], Hq, *cache, *tables, token_idx.data_ptr(), ts[0], width, T, gate_p, scale,
@@ -679,6 +679,7 @@ def accumulate_weights(weights: torch.Tensor, token_idx: torch.Tensor, page_tabl
     return token_weight
 
 
+@functools.lru_cache(maxsize=1024)
 def evict_pages_workspace_size(R: int, max_pages: int, page_size: int) -> int:
     return int(lib().qsa_evict_pages_workspace_size(R, max_pages, page_size))
 
@@ -717,7 +718,7 @@ def evict_pages(token_weight: torch.Tensor, page_table: torch.Tensor, seq_lens: 
                 raise ValueError(f"{n} must be int32 [R, max_pages] with unit column stride")
         out0, freed0 = table_out.stride(0), freed.stride(0)
     if counts is None:
-        counts = _new(stream, (R,), torch.int32, dev)
+        counts = _new(stream, R, torch.int32, dev)
     else:
         _want(counts, "counts", torch.int32, 1, dev)
         if counts.shape[0] != R or not counts.is_contiguous():
