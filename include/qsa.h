@@ -445,15 +445,16 @@ size_t qsa_mqa_paged_batch_workspace_size(int32_t R, int32_t num_decodes, int32_
  *              or heads outermost inside a page, and K and V interleaved in
  *              one pool, are all strides.
  *   k_scale,   fp32 [num_pages, page_size / block_tokens, Hkv]: page and
- *   v_scale    block strides in elements, unit head stride; > 0 and finite
- *              for every block that holds a token.  A k_scale of 0 (memory
- *              zeroed once) marks a block and head that holds none: attention
- *              does not see its tokens.
+ *   v_scale    block strides in elements, unit head stride; >= 2^-126 and
+ *              finite for every block that holds a token.  A k_scale of 0
+ *              (memory zeroed once) marks a block and head that holds none:
+ *              attention does not see its tokens, whatever their codes are.
  *   block_tokens  1 .. page_size, dividing page_size (any page_size >= 1).
  * The pages' K/V cache is 16-bit; this one halves its memory and traffic.
  * Requests, rows and page tables are those of qsa_sparse_attention: row i of
  * request r sits at logical position seq_lens[r] - qlen_r + i, entries of
- * page_table outside [0, num_pages) are missing pages.  Rows at or behind
+ * page_table outside [0, num_pages) are missing pages.  Rows in front of
+ * cu_seqlens_q[0] (requests that are a slice of the batch) and at or behind
  * cu_seqlens_q[R] (a padded batch) belong to no request.
  */
 

@@ -312,12 +312,14 @@ __device__ __forceinline__ uint16_t narrow(float x) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// attn::row_request, with position -1 (nothing visible) for the rows behind
-// the last request's: a batch may be padded.
+// attn::row_request, with position -1 (nothing visible) for the rows in front of
+// the first request's and behind the last one's: the requests may be a slice of
+// the batch, and a batch may be padded.
 __device__ __forceinline__ void row_position(const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_lens,
                                              int R, int64_t t, int lane, int& r, int& pos, int& L) {
-  attn::row_request(cu, seq_lens, R, t, lane, r, pos, L);
-  if (t >= (int64_t)__ldg(cu + r + 1)) pos = -1;
+  const int64_t begin = __ldg(cu);                     // row_request counts on a request that begins at or before t
+  attn::row_request(cu, seq_lens, R, max(t, begin), lane, r, pos, L);
+  if (t < begin || t >= (int64_t)__ldg(cu + r + 1)) pos = -1;
 }
 
 // The entries of consecutive tiles, looked up in stages so that no load is
@@ -504,18 +506,23 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       return true;
     };
     int row_v = -1;                                    // the last tile's row, whose V is still to come
+    float held_v = 0.f;                                // and its k_scale: V codes of a block that holds nothing may
+                                                       // be NaN, which no probability of 0 would hide
+    auto gather_v = [&](int tile) { return gather(p.v, held_v != 0.f ? row_v : -1, tile, -1); };
     bool ok = true;
     for (int k = 0; k < n; ++k) {
       int page, j, g;
       f.next(p, page, j, g);
       const int in_page = j - divide(j, p.by_page) * p.page_size;
       const int row = page < 0 ? -1 : page * p.page_rows + in_page * p.token_rows + g * p.head_rows;
-      const int64_t at = C::RING && row >= 0 ? scale_index(p, page, in_page, g) : 0;
-      ok = gather(p.k, row, k, at) && (k == 0 || gather(p.v, row_v, k - 1, -1));
+      const int64_t at = row >= 0 ? scale_index(p, page, in_page, g) : 0;
+      const float held = row >= 0 ? __ldg(p.k_scale + at) : 0.f;
+      ok = gather(p.k, row, k, at) && (k == 0 || gather_v(k - 1));
       if (!ok) break;
       row_v = row;
+      held_v = held;
     }
-    if (!ok || !gather(p.v, row_v, n - 1, -1)) gone();
+    if (!ok || !gather_v(n - 1)) gone();
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 8) {
     if constexpr (C::RESIDENT > 1) regs_shrink<REGS_REST>();
@@ -813,7 +820,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         named_barrier_sync(2, SOFT);                   // red_s may be written again
       }
       if constexpr (!C::RING) scales();                // of tile k + 1
-      // ---- P times v_scale / vref as three E4M3 terms
+      // ---- P times v_scale / vref as four E4M3 terms
       const float2 vn = both(vs * vinv);
       uint32_t w4[PN / 4];
 #pragma unroll

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendP
   // blocks do not cross pages: bt divides page_size
   const int64_t a = max(p0, (int64_t)0);
   const int64_t block0 = (a / bt + nth) * bt;       // first token of this block
-  if (block0 >= L) return;
+  if (nth < 0 || block0 >= L) return;               // nth < 0: rows in front of the first request's
   const int64_t begin = max(block0, a);
   const int n_new = (int)(min(block0 + bt, (int64_t)L) - begin);
   const int n_old = (int)(begin - block0);
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_kernel(const Ev
   int32_t* out = p.table_out + (int64_t)r * p.out_stride;
   int32_t* freed = p.freed + (int64_t)r * p.freed_stride;
   const unsigned long long* keys = FORM == FROM_WORKSPACE ? p.key + (int64_t)r * p.max_pages : key_s;
-  const int want_keep = __ldg(p.keep + r);
+  const int want_keep = max(0, __ldg(p.keep + r));
   auto is_live = [&](int lp, int entry) { return lp < n && entry >= 0 && entry < p.num_pages; };
   auto is_held = [&](int lp) { return lp < p.keep_first || lp >= n - p.keep_last; };
 

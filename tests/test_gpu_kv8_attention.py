@@ -251,6 +251,34 @@ def test_blocks_that_hold_nothing_are_not_seen():
         check(d, gpu(d))
 
 
+def test_nan_codes_of_blocks_that_hold_nothing_do_not_show():
+    """Pools whose scales alone were zeroed: the codes of blocks never written may be NaN."""
+    for Hq, dtype in ((24, torch.bfloat16), (32, torch.bfloat16), (24, torch.float16), (32, torch.float16)):
+        d = make([300, 400], [2, 3], Hq, 2, 16, 8, 300, seed=20, dtype=dtype)
+        d["ks"][d["table"][:, 1].long(), 1] = 0
+        d["ks"][d["table"][:, 3].long(), :, 0] = 0
+        want = gpu(d)
+        for c in ("kc", "vc"):
+            b = d[c].view(-1, 2, 8, 2, 256)
+            b[(d["ks"] == 0)[:, :, None, :].expand(-1, -1, 8, -1)] = 255
+        got = gpu(d)
+        check(d, got)
+        assert all(np.array_equal(a, b) for a, b in zip(want, got))
+
+
+def test_rows_in_front_of_the_first_request_belong_to_none():
+    """The requests of a batch's tail with the whole batch's rows."""
+    d = make([300, 65, 90], [2, 5, 1], 24, 2, 16, 16, 60, seed=21)
+    tail = dict(d, cu=d["cu"][1:], sl=d["sl"][1:], table=d["table"][1:])
+    got = gpu(tail)
+    check(tail, got)
+    assert np.all(np.isneginf(got[1][:2])) and np.all(got[0][:2] == 0) and np.all(got[2][:2] == 0)
+    assert all(np.array_equal(a[2:], b[2:]) for a, b in zip(gpu(d), got))
+    for n in (1, 2, 5):                              # and one request alone
+        last = dict(d, cu=d["cu"][2:], sl=d["sl"][2:], table=d["table"][2:], q=d["q"][:n], tok=d["tok"][:n])
+        assert np.all(np.isneginf(gpu(last)[1]))
+
+
 @pytest.mark.parametrize("rows,width", [(600, 300), (90, 1500)])
 def test_many_rows(rows, width):
     """Runs of whole lists (600 rows of 3 tiles) and runs that cut lists (90 rows of 12 tiles)."""

@@ -116,6 +116,18 @@ def test_append_padded_batch_and_short_requests():
     check_append(d, gpu_append(d))
 
 
+@pytest.mark.parametrize("bt", [1, 4, 16])
+def test_append_rows_in_front_of_the_first_request(bt):
+    """The requests of a batch's tail with the whole batch's rows: the head's are written nowhere."""
+    d = append_inputs([40, 3, 90, 31], [20, 2, 33, 31], 2, 16, bt, seed=8)
+    for n in (1, 2, 3):
+        tail = dict(d, cu=d["cu"][n:], sl=d["sl"][n:], table=d["table"][n:])
+        tail["ks"] = torch.zeros_like(d["ks"])       # (old scales of 0: a write to a wrong block would show)
+        tw = torch.ones((d["kc"].shape[0], 16), dtype=torch.int64)
+        got_tw = tw.to(DEV)
+        check_append(tail, gpu_append(tail, got_tw), tw, got_tw)
+
+
 def test_append_layouts():
     d = append_inputs([70, 5, 200], [4, 3, 2], 2, 64, 16, seed=9)
     want = gpu_append(d)
@@ -218,6 +230,19 @@ def test_accumulate_strides_padding_and_empty():
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+def test_accumulate_rows_in_front_of_the_first_request():
+    table, sl, cu, pages = ref.layout([90, 50, 33], [3, 2, 4], 16, 6)
+    tok = ref.token_lists([90, 50, 33], [3, 2, 4], 40, 7)
+    w = torch.rand((9, 40))
+    for n in (1, 2):
+        want = np.zeros((pages, 16), np.int64)
+        ref.accumulate(w.double().numpy(), tok.numpy(), table[n:].numpy(), cu[n:].numpy(), sl[n:].numpy(), want)
+        got = torch.zeros((pages, 16), dtype=torch.int64, device=DEV)
+        qsa.accumulate_weights(w.to(DEV), tok.to(DEV), table[n:].to(DEV), cu[n:].to(DEV), sl[n:].to(DEV), got)
+        torch.cuda.synchronize()
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 # ------------------------------------------------------------------ eviction
 
 def gpu_evict(tw, table, sl, keep, first, last, **kw):
@@ -240,6 +265,18 @@ def test_evict_matches_reference(ps, first, last):
         want = ref.evict(tw.numpy(), table.numpy(), sl.numpy(), keep.numpy(), first, last)
         got = gpu_evict(tw, table, sl, keep, first, last)
         assert all(np.array_equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("tokens", [400, 90000])
+def test_evict_extreme_counts(tokens):
+    table, sl, cu, pages = ref.layout([tokens, tokens - 5, 30], [1, 1, 1], 16, 9)
+    tw = torch.randint(0, 1 << 30, (pages, 16), generator=torch.Generator().manual_seed(2))
+    for keep in (-2 ** 31, -1, 2 ** 31 - 1):
+        k = torch.full((3,), keep, dtype=torch.int32)
+        for first, last in ((2, 1), (2 ** 31 - 1, 0), (0, 2 ** 31 - 1)):
+            want = ref.evict(tw.numpy(), table.numpy(), sl.numpy(), k.numpy(), first, last)
+            got = gpu_evict(tw, table, sl, k, first, last)
+            assert all(np.array_equal(a, b) for a, b in zip(got, want))
 
 
 def test_evict_ties_keep_the_earlier_pages():
