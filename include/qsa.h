@@ -517,8 +517,8 @@ qsa_status_t qsa_kv_append_fp8_f16(const void* k, int64_t k_stride_t, int64_t k_
  * QSA_ERR_UNSUPPORTED when the cache spans 2^31 - 1 or more multiples of the
  * greatest common divisor of its strides (512 GiB at a divisor of 256), or
  * T * Hkv * ceil(width / 128) exceeds 2^30.  A query head with a NaN or infinite
- * element gives NaN.  One launch, a second one where a row's list is cut
- * between thread blocks, and a last one for the weights.
+ * element gives NaN.  One launch, and a second one for the weights or where a
+ * row's list is cut between thread blocks.
  */
 qsa_status_t qsa_sparse_attention_fp8(const void* q, int64_t q_stride_t, int64_t q_stride_h, int32_t Hq,
                                       const void* k_cache, const void* v_cache, const float* k_scale,

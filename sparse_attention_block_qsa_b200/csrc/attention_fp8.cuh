@@ -29,7 +29,7 @@
 // Work is the list of (row, KV head, 128-entry tile) triples in order; every CTA
 // takes an equal contiguous run of it (two CTAs per SM), so any batch fills the
 // GPU to one tile.  A run may begin and end inside a row's list: such pieces go
-// to the workspace and combine_fp8_kernel merges them.  Inside a CTA
+// to the workspace and finish_fp8_kernel merges them.  Inside a CTA
 //  * warps 4-7 look entries up (list, page table) and gather their K and V rows
 //    with 16-byte cp.async into three 32 KB buffers that K and V tiles take in
 //    turn.  (TMA gathers are no match here: measured 10.7 cycles a 128-byte row
@@ -149,18 +149,25 @@ struct Params {
   float scale_log2;
   float* part_o;              // [2 ctas, group, 256] unnormalised outputs of pairs cut by a run's ends
   float* part_ml;             // [2 ctas, group, 2] maximum (log2 units), sum
-  float* part_s;              // [T, Hkv, width, group] scores (log2 units), or null
-  float* lse2;                // [T, Hq] log2 of the sum of 2^s, or null
+  float* part_s;              // [T, Hq, width] scores (log2 units), or null
+  float* lse2;                // [T, Hq] log2 of the sum of 2^s (of pairs that no run cuts), or null
   const float* gate;
   uint16_t* out;
   int64_t out_st;
   float* lse;
   float* weights;             // [T, width], or null
   int64_t w_stride;
+  // the second launch: CTAs that add probabilities up, then `places` (pairs or cuts, whatever is fewer) per 2 heads
+  int32_t sums, places;
 };
 
 // First tile of run i.
 __device__ __forceinline__ int run_begin(const Params& p, int i) { return (i * p.per + min(i, p.more)) * p.unit; }
+// The run that holds tile u.
+__device__ __forceinline__ int run_of(const Params& p, int u) {
+  const int v = u / p.unit, longer = p.more * (p.per + 1);
+  return v < longer ? v / (p.per + 1) : p.more + (v - longer) / p.per;
+}
 
 // Whether the phase with the given parity has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -765,10 +772,10 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       if (p.part_s) {
         const int e = tile * TILE + tid;
         if (e < p.width) {
-          float* dst = p.part_s + ((int64_t)pair * p.width + e) * p.group;
+          float* dst = p.part_s + (int64_t)pair * p.group * p.width + e;
 #pragma unroll
           for (int h = 0; h < HG; ++h)
-            if (h < p.group) dst[h] = h & 1 ? x[h / 2].y - nref[h / 2].y : x[h / 2].x - nref[h / 2].x;
+            if (h < p.group) dst[(int64_t)h * p.width] = h & 1 ? x[h / 2].y - nref[h / 2].y : x[h / 2].x - nref[h / 2].x;
         }
       }
       float over = -INFINITY;
@@ -925,25 +932,96 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
   if (warp == 8) tmem_dealloc(tmem, C::TMEM);
 }
 
-// Merges the pieces of pairs cut by the end of a run: one CTA per (cut, 2
-// heads), two features a thread.  The CTAs of a pair's first cut merge all of its
-// pieces.  It is launched while the attention runs and waits for it.
+// What follows the attention, in one launch that waits for it.  Its first CTAs add
+// the probabilities up over the query heads, 256 entries of a row each; the
+// others merge the pieces of pairs cut by the end of a run, two features a thread
+// and 2 heads a CTA.  The first work a cut pair's sums out of its pieces again,
+// instead of waiting for the merge in a launch of their own.
 constexpr int MERGE_HEADS = 2, MERGE_THREADS = MERGE_HEADS * D / 2;
 
+// weights[t, e] = sum over query heads of 2^(s - lse2): one thread per entry, heads in order.
+template <int BATCH>
+__device__ __forceinline__ void add_probabilities(const Params& p, int block) {
+  const int per_row = (p.width + MERGE_THREADS - 1) / MERGE_THREADS;
+  const int t = block / per_row, e = (block - t * per_row) * MERGE_THREADS + (int)threadIdx.x, lane = threadIdx.x & 31;
+  const bool in = e < p.width;
+  float w = 0.f;
+  for (int g = 0; g < p.Hkv; ++g) {
+    const int pair = t * p.Hkv + g, begin = pair * p.tiles, end = begin + p.tiles;
+    const float* s = p.part_s + (int64_t)pair * p.group * p.width + e;
+    float x[MAX_GROUP];                                // on their way while the sums are worked out
+#pragma unroll
+    for (int h = 0; h < MAX_GROUP; ++h) x[h] = in && h < p.group ? s[(int64_t)h * p.width] : -INFINITY;
+    const int first = run_of(p, begin);
+    float l2 = 0.f;                                    // of head `lane`
+    if (lane < p.group) {
+      if (run_begin(p, first + 1) >= end) {
+        l2 = p.lse2[(int64_t)pair * p.group + lane];
+      } else {
+        float M = -INFINITY, sum = 0.f;
+        for (int i0 = first; i0 < p.ctas && run_begin(p, i0) < end; i0 += BATCH) {
+          float2 ml[BATCH];
+          float m = M;
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int run = i0 + i;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (run < p.ctas && run_begin(p, run) < end) {
+              const int64_t slot = 2 * (int64_t)run + (run == first && run_begin(p, run) < begin ? 1 : 0);
+              ml[i] = reinterpret_cast<const float2*>(p.part_ml)[slot * p.group + lane];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) m = fmaxf(m, ml[i].x);
+          const float mr = m == -INFINITY ? 0.f : m;
+          sum *= exp2f(M - mr);
+          M = m;
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) sum = fmaf(exp2f(ml[i].x - mr), ml[i].y, sum);
+        }
+        l2 = sum == 0.f ? -INFINITY : M + log2f(sum);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < MAX_GROUP; ++h) {
+      const float l = __shfl_sync(0xffffffffu, l2, h);
+      w += x[h] == -INFINITY ? 0.f : exp2f(x[h] - l);
+    }
+  }
+  if (in) p.weights[t * p.w_stride + e] = w;
+}
+
 template <bool F16, int BATCH>   // pieces loaded in one round trip
-__global__ void __launch_bounds__(MERGE_THREADS) combine_fp8_kernel(const Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int cut = blockIdx.x + 1;                      // between runs cut - 1 and cut
-  const int hh = blockIdx.y * MERGE_HEADS + threadIdx.x / (D / 2), f2 = threadIdx.x % (D / 2);
-  const int at = run_begin(p, cut), pair = at / p.tiles, begin = pair * p.tiles, first = cut - 1;
-  // no cut inside a pair, or not the pair's first one
-  if (at == begin || (first > 0 && run_begin(p, first) > begin) || hh >= p.group) return;
+__global__ void __launch_bounds__(MERGE_THREADS) finish_fp8_kernel(const Params p) {
+  const int block = (int)blockIdx.x - p.sums;
+  if (block < 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    add_probabilities<BATCH>(p, (int)blockIdx.x);
+    return;
+  }
+  const int heads = block / p.places, place = block - heads * p.places;
+  const int hh = heads * MERGE_HEADS + threadIdx.x / (D / 2), f2 = threadIdx.x % (D / 2);
+  int pair, begin, first;
+  bool mine;
+  if (p.places < p.ctas - 1) {                         // fewer pairs than cuts: a CTA per pair
+    pair = place;
+    begin = pair * p.tiles;
+    first = run_of(p, begin);
+    mine = run_begin(p, first + 1) < begin + p.tiles;
+  } else {                                             // a CTA per cut, between runs `place` and place + 1
+    first = place;
+    const int at = run_begin(p, first + 1);
+    pair = at / p.tiles;
+    begin = pair * p.tiles;
+    mine = at > begin && (first == 0 || run_begin(p, first) <= begin);   // inside a pair, and its first cut
+  }
   int pieces = 2;
   while (first + pieces < p.ctas && run_begin(p, first + pieces) < begin + p.tiles) ++pieces;
   // the first piece ends run `first` (its second slot unless the run begins with this pair); the others begin theirs
   const int slot0 = 2 * first + (run_begin(p, first) >= begin ? 0 : 1);
   auto slot = [&](int i) { return (int64_t)(i == 0 ? slot0 : 2 * (first + i)) * p.group + hh; };
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // every CTA: the grid must not end before the attention does
+  if (!mine || hh >= p.group) return;
   // (plain loads: the pieces are written while this grid is already launched)
   float M = -INFINITY, sum = 0.f;
   float2 acc = make_float2(0.f, 0.f);
@@ -983,28 +1061,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine_fp8_kernel(const Params
   if (f2 == 0) {
     const float l2 = sum == 0.f ? -INFINITY : M + log2f(sum);
     if (p.lse) p.lse[t * p.Hq + h] = l2 * 0.69314718055994531f;
-    if (p.lse2) p.lse2[t * p.Hq + h] = l2;
   }
-}
-
-// weights[t, e] = sum over query heads of 2^(s - lse2): one thread per entry,
-// heads in order.
-__global__ void __launch_bounds__(256) weights_kernel(const Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t t = blockIdx.y;
-  const int e = (int)(blockIdx.x * blockDim.x + threadIdx.x);
-  if (e >= p.width) return;
-  float w = 0.f;
-  for (int g = 0; g < p.Hkv; ++g) {
-    const float* s = p.part_s + ((t * p.Hkv + g) * p.width + e) * p.group;
-    const float* l = p.lse2 + t * p.Hq + g * p.group;
-#pragma unroll 4
-    for (int h = 0; h < p.group; ++h) {
-      const float x = s[h];
-      w += x == -INFINITY ? 0.f : exp2f(x - l[h]);
-    }
-  }
-  p.weights[t * p.w_stride + e] = w;
 }
 
 }  // namespace attn8

@@ -1266,14 +1266,13 @@ size_t qsa_sparse_attention_fp8_workspace_size(int64_t T, int32_t Hq, int32_t Hk
 extern "C++" {
 template <bool F16, int HG>
 static void launch_attn8(const qsa::attn8::Params& p, cudaStream_t s) {
-  qsa::attn8::attn_fp8_kernel<F16, HG><<<(unsigned)p.ctas, qsa::attn8::THREADS, qsa::attn8::Cfg<F16, HG>::SMEM, s>>>(p);
-  if (p.ctas > 1 && p.unit < p.tiles) {                     // runs may end inside a pair
-    const dim3 grid((unsigned)p.ctas - 1, (unsigned)((p.group + qsa::attn8::MERGE_HEADS - 1) / qsa::attn8::MERGE_HEADS));
-    const dim3 threads(qsa::attn8::MERGE_THREADS);
-    // a pair of `tiles` tiles has at most (tiles - 2) / per + 2 pieces
-    if ((p.tiles - 2) / p.per + 2 <= 4) launch_pdl(qsa::attn8::combine_fp8_kernel<F16, 4>, grid, threads, 0, s, p);
-    else launch_pdl(qsa::attn8::combine_fp8_kernel<F16, 18>, grid, threads, 0, s, p);
-  }
+  using namespace qsa::attn8;
+  attn_fp8_kernel<F16, HG><<<(unsigned)p.ctas, THREADS, Cfg<F16, HG>::SMEM, s>>>(p);
+  const dim3 grid((unsigned)(p.sums + p.places * ((p.group + MERGE_HEADS - 1) / MERGE_HEADS))), threads(MERGE_THREADS);
+  if (grid.x == 0) return;
+  // a pair of `tiles` tiles has at most (tiles - 2) / per + 2 pieces
+  if (p.places == 0 || (p.tiles - 2) / p.per + 2 <= 4) launch_pdl(finish_fp8_kernel<F16, 4>, grid, threads, 0, s, p);
+  else launch_pdl(finish_fp8_kernel<F16, 18>, grid, threads, 0, s, p);
 }
 }  // extern "C++"
 
@@ -1404,6 +1403,8 @@ static qsa_status_t attention_fp8_common(
   p.lse = lse;
   p.weights = want_w ? weights : nullptr;
   p.w_stride = T > 1 ? weights_stride : width;
+  p.sums = want_w ? (int32_t)(T * ((width + MERGE_THREADS - 1) / MERGE_THREADS)) : 0;
+  p.places = whole ? 0 : (int32_t)std::min<int64_t>(p.ctas - 1, all_pairs);   // runs may end inside a pair
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (f16) {
     if (HG == 8) launch_attn8<true, 8>(p, s);
@@ -1413,15 +1414,6 @@ static qsa_status_t attention_fp8_common(
     if (HG == 8) launch_attn8<false, 8>(p, s);
     else if (HG == 12) launch_attn8<false, 12>(p, s);
     else launch_attn8<false, 16>(p, s);
-  }
-  // rows in grid y, at most 65,535 a launch
-  for (int64_t r0 = 0; want_w && r0 < T; r0 += 65535) {
-    const int64_t rows_w = std::min<int64_t>(T - r0, 65535);
-    Params pw = p;
-    pw.part_s += r0 * Hkv * width * p.group;
-    pw.lse2 += r0 * Hq;
-    pw.weights += r0 * p.w_stride;
-    launch_pdl(weights_kernel, dim3((unsigned)((width + 255) / 256), (unsigned)rows_w), dim3(256), 0, s, pw);
   }
   return launch_status("8-bit cache attention kernels");
 }
