@@ -277,17 +277,18 @@ __device__ __forceinline__ void weigh(const EvictParams& p, const int (&page)[WE
   for (int b = 0; b < WEIGH_EACH; ++b) v[b] = 0;
   constexpr int STEP = PAIRS ? 2 : 1;
   for (int e = STEP * sub; e < p.page_size; e += STEP * lanes) {
+    ulonglong2 x[WEIGH_EACH];                          // all loads before the sums
 #pragma unroll
     for (int b = 0; b < WEIGH_EACH; ++b) {
-      if (page[b] < 0) continue;
       const int64_t* w = p.token_weight + (int64_t)page[b] * p.page_size + e;
-      if (PAIRS) {
-        const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2*>(w));
-        v[b] += x.x + x.y;
-      } else {
-        v[b] += __ldg(reinterpret_cast<const unsigned long long*>(w));
+      x[b] = make_ulonglong2(0, 0);
+      if (page[b] >= 0) {
+        if (PAIRS) x[b] = __ldg(reinterpret_cast<const ulonglong2*>(w));
+        else x[b].x = __ldg(reinterpret_cast<const unsigned long long*>(w));
       }
     }
+#pragma unroll
+    for (int b = 0; b < WEIGH_EACH; ++b) v[b] += x[b].x + x[b].y;
   }
   int first = 0, held = WEIGH_EACH, o = lanes >> 1;    // this lane holds pages first .. first + held - 1
 #pragma unroll
