@@ -467,7 +467,8 @@ size_t qsa_mqa_paged_batch_workspace_size(int32_t R, int32_t num_decodes, int32_
  *     s'   = need                  if the block's first token is among them
  *          = max(s, need)          otherwise (s: the block's scale so far)
  * New elements become E4M3(x / s') (nearest even; NaN stays NaN, infinities
- * become +-448).  If s' != s the block's tokens in front of the first new row
+ * become +-448; with a scale of another writer that is no power of two, the
+ * quotient is rounded to fp32 first).  If s' != s the block's tokens in front of the first new row
  * become E4M3(E4M3 value * s / s').  Tokens behind the last new row are left
  * as they are: they are not part of the request any more (rejected
  * speculative tokens are overwritten this way).  Rows whose page is missing or

@@ -1,7 +1,7 @@
 // The 8-bit K/V cache around its attention: appending new tokens, adding
 // attention weights up per cached token, dropping the lightest pages.
 //
-//  * append_kernel: one CTA per (scale block, KV head, K or V).  A block's
+//  * append_kernel: one CTA, or for small blocks one warp, per (scale block, KV head, K or V).  A block's
 //    scale is the smallest power of two that holds its largest element
 //    (amax <= 448 s), so the codes lose nothing to the scale, a grown scale
 //    moves old codes by whole exponents (only what falls below E4M3's
@@ -78,17 +78,19 @@ __device__ __forceinline__ uint2 encode8(const float* x) {
                     attn8::e4m3x2(x[4], x[5]) | (attn8::e4m3x2(x[6], x[7]) << 16));
 }
 
+// (out of line: eight of them in every store would make the kernel's code slower to fetch than its data)
+__device__ __noinline__ float quotient(float a, float b) { return a / b; }
+
 // Slots of scale blocks: request r owns slots cu[r] / bt + 2 r onwards, which
 // are enough (qlen rows touch at most qlen / bt + 2 blocks).  Up to HELD rows a
 // warp stay in registers between the maximum and the quantisation; the rows of
-// larger blocks are read again (out of L1 or L2).
-constexpr int HELD = 4;
-
-template <bool F16>
+// longer blocks (LONG) are read again, out of L1 or L2.  Little code matters: the
+// kernel runs for a few microseconds, much of it while instructions are fetched.
+template <bool F16, int WARPS, int HELD, bool LONG>   // warps a block: all of the CTA's or one
 __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendParams p) {
   __shared__ float top_s[APPEND_WARPS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t slot = blockIdx.x;
+  const int warp = WARPS == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t slot = WARPS == 1 ? (int64_t)blockIdx.x * APPEND_WARPS + (threadIdx.x >> 5) : blockIdx.x;
   const int h = blockIdx.y, which = blockIdx.z;
   const int bt = p.block_tokens;
   // the last request whose slots begin at or before this one, 32 candidates a round trip
@@ -114,10 +116,14 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendP
   const int n_old = (int)(begin - block0);
   const int64_t x_st = p.x_st[which];
   const uint16_t* x = p.x[which] + (first + (begin - p0)) * x_st + h * p.x_sh[which] + lane * 8;
-  uint4 row[HELD];
+  constexpr int ROUND = HELD * WARPS;               // rows in flight at once
+  auto load = [&](int from, uint4 (&to)[HELD]) {
 #pragma unroll
-  for (int i = 0; i < HELD; ++i)
-    if (warp + i * APPEND_WARPS < n_new) row[i] = __ldg(reinterpret_cast<const uint4*>(x + (warp + i * APPEND_WARPS) * x_st));
+    for (int i = 0; i < HELD; ++i)
+      if (from + i * WARPS < n_new) to[i] = __ldg(reinterpret_cast<const uint4*>(x + (from + i * WARPS) * x_st));
+  };
+  uint4 row[HELD];
+  load(warp, row);
   const int lp = (int)block0 / p.page_size;
   const int page = lp < p.max_pages ? __ldg(p.page_table + (int64_t)r * p.pt_stride + lp) : -1;
   if (page < 0 || page >= p.num_pages) return;      // no page: the tokens are dropped
@@ -139,20 +145,32 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendP
   };
 #pragma unroll
   for (int i = 0; i < HELD; ++i)
-    if (warp + i * APPEND_WARPS < n_new) measure(row[i]);
-  for (int i = warp + HELD * APPEND_WARPS; i < n_new; i += APPEND_WARPS)
-    measure(__ldg(reinterpret_cast<const uint4*>(x + i * x_st)));
-  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-  if (lane == 0) top_s[warp] = attn8::widen2<F16>(top).x;
-  __syncthreads();
-  float amax = 0.f;
+    if (warp + i * WARPS < n_new) measure(row[i]);
+  if (LONG) {
+#pragma unroll 1
+    for (int from = warp + ROUND; from < n_new; from += ROUND) {
+      uint4 more[HELD];                               // read again below, out of L1 or L2
+      load(from, more);
 #pragma unroll
-  for (int w = 0; w < APPEND_WARPS; ++w) amax = fmaxf(amax, top_s[w]);
+      for (int i = 0; i < HELD; ++i)
+        if (from + i * WARPS < n_new) measure(more[i]);
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+  float amax = 0.f;
+  if (WARPS == 1) {
+    amax = attn8::widen2<F16>(top).x;
+  } else {
+    if (lane == 0) top_s[warp] = attn8::widen2<F16>(top).x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, top_s[w]);
+  }
   const float s = fmaxf(before, __uint_as_float((uint32_t)(scale_exponent(amax) + 127) << 23));
-  if (threadIdx.x == 0 && s != before) *sc = s;
+  if (warp == 0 && lane == 0 && s != before) *sc = s;
   if (n_old > 0 && s != before) {
     const float ratio = before / s;
-    for (int i = warp; i < n_old; i += APPEND_WARPS) {
+    for (int i = warp; i < n_old; i += WARPS) {
       uint2* at = reinterpret_cast<uint2*>(rows + i * p.kv_row_stride);
       const uint2 c = *at;
       float f[8];
@@ -171,16 +189,23 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) append_kernel(const AppendP
     float f[8];
     widen8<F16>(v, f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = pow2 ? f[k] * inv : f[k] / s;
+    for (int k = 0; k < 8; ++k) f[k] = pow2 ? f[k] * inv : quotient(f[k], s);
     *reinterpret_cast<uint2*>(rows + (int64_t)(n_old + i) * p.kv_row_stride) = encode8(f);
   };
 #pragma unroll
   for (int i = 0; i < HELD; ++i)
-    if (warp + i * APPEND_WARPS < n_new) store(warp + i * APPEND_WARPS, row[i]);
-  for (int i = warp + HELD * APPEND_WARPS; i < n_new; i += APPEND_WARPS)
-    store(i, __ldg(reinterpret_cast<const uint4*>(x + i * x_st)));
+    if (warp + i * WARPS < n_new) store(warp + i * WARPS, row[i]);
+  if (LONG) {
+#pragma unroll 1
+    for (int from = warp + ROUND; from < n_new; from += ROUND) {
+      load(from, row);
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (from + i * WARPS < n_new) store(from + i * WARPS, row[i]);
+    }
+  }
   if (p.token_weight && h == 0 && which == 0)
-    for (int i = threadIdx.x; i < n_new; i += blockDim.x)
+    for (int i = 32 * warp + lane; i < n_new; i += 32 * WARPS)
       p.token_weight[(int64_t)page * p.page_size + in_page + n_old + i] = 0;
 }
 

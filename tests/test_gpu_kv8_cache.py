@@ -116,6 +116,41 @@ def test_append_padded_batch_and_short_requests():
     check_append(d, gpu_append(d))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("ps,bt", [(8, 2), (12, 3), (16, 4), (10, 5), (14, 7), (16, 8), (18, 9), (51, 17)])
+def test_append_many_small_blocks(ps, bt, dtype):
+    """Blocks that a warp takes, some with tokens in front, in requests of all alignments and in large numbers."""
+    seq_lens, qlens = [450, 333, 5, 40, 9, 21], [450, 331, 2, 1, 4, 3]
+    d = append_inputs(seq_lens, qlens, 4, ps, bt, seed=ps, dtype=dtype, spread=2.0)
+    tw = torch.ones((d["kc"].shape[0], ps), dtype=torch.int64)
+    got_tw = tw.to(DEV)
+    check_append(d, gpu_append(d, got_tw), tw, got_tw)
+    few = append_inputs(seq_lens[2:], qlens[2:], 1, ps, bt, seed=ps + 1, dtype=dtype, spread=2.0)
+    check_append(few, gpu_append(few))
+
+
+def test_append_behind_scales_that_are_no_powers_of_two(monkeypatch):
+    """A block begun with another writer's scale keeps it while it is large enough.  What becomes a code is rounded to
+    fp32 on the way: x / s once, an older value times s / s' twice (the ratio and the product), 2^-24 relative each.
+    So a code is that of a value within 2^-23 of the exact one.  (With s = 1.3 * 2^n this does happen: 2.03125 / 1.3 =
+    25 / 16 lies in the middle of two codes, and the fp32 value of 1.3 is 4e-8 below it.)"""
+    exact = ref.encode
+    for ps, bt in ((16, 16), (64, 64), (16, 4), (16, 8)):
+        d = append_inputs([70, 40, 90, 31], [2, 1, 3, 2], 2, ps, bt, seed=15, spread=0.2)
+        d["ks"], d["vs"] = d["ks"] * 1.3, d["vs"] * 37.7
+        got = gpu_append(d)
+        for x, c, n in (("k", "kc", "ks"), ("v", "vc", "vs")):
+            either = []
+            for off in (1 - 2.0 ** -23, 1 + 2.0 ** -23):
+                monkeypatch.setattr(ref, "encode", lambda v: exact(np.asarray(v) * off))
+                codes, scales = d[c].clone().numpy(), d[n].double().numpy().copy()
+                ref.append(d[x].double().numpy(), codes, scales, d["table"].numpy(), d["cu"].numpy(), d["sl"].numpy())
+                either.append(codes)
+            assert np.array_equal(got[n].double().numpy(), scales)
+            assert np.any(scales != 2.0 ** np.round(np.log2(scales)))
+            assert np.all((got[c].numpy() == either[0]) | (got[c].numpy() == either[1]))
+
+
 @pytest.mark.parametrize("bt", [1, 4, 16])
 def test_append_rows_in_front_of_the_first_request(bt):
     """The requests of a batch's tail with the whole batch's rows: the head's are written nowhere."""
