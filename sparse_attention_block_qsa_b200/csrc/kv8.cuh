@@ -6,8 +6,8 @@
 //    (amax <= 448 s), so the codes lose nothing to the scale, a grown scale
 //    moves old codes by whole exponents (only what falls below E4M3's
 //    normal range is rounded again), and attention reads back exact products.
-//    Bound by the chain lengths -> rows and page -> scale (3.0 us for 16 tokens)
-//    and, for many rows, by how many CTAs hide it: 8,192 rows 9.5 us (25 MB).
+//    Bound by the chain lengths -> rows and page -> scale (2.9 us for 16 tokens)
+//    and, for many rows, by how many CTAs hide it: 8,192 rows 8.2 us (25 MB).
 //  * accumulate_kernel: a warp per run of a row's list entries.  Weights are
 //    counted in units of 2^-32 in 64-bit integers: the order of the atomics
 //    cannot change the sums.  4.2 M entries take 13.6 us, whatever a warp holds:

@@ -1401,10 +1401,11 @@ static qsa_status_t attention_fp8_common(
   if (total > INT32_MAX / 2) return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
   const int HG = p.group <= 8 ? 8 : p.group <= 12 ? 12 : 16;   // query heads the kernel holds
   p.ctas = (int32_t)std::min(total, f16 && HG == 16 ? kAttn8Runs / 2 : kAttn8Runs);
-  // Whole pairs for every run where that makes no run more than 3 tiles longer (about 6 us, what merging the pieces of
-  // cut pairs costs: 4.4 to 8 us measured); else runs equal to one tile.
+  // Whole pairs for every run where that makes no run more than 4 tiles longer (24 / 2 heads, 17 tiles a pair: 1 tile
+  // longer 60.6 us against 65.5 with cut pairs and their merge, 4 longer 60.0 and 61.7, 5 longer 60.0 and 60.4); else runs
+  // equal to one tile.
   const int64_t all_pairs = T * Hkv, most = (all_pairs + p.ctas - 1) / p.ctas;
-  const bool whole = p.tiles == 1 || most * p.tiles - (total + p.ctas - 1) / p.ctas <= 3;
+  const bool whole = p.tiles == 1 || most * p.tiles - (total + p.ctas - 1) / p.ctas <= 4;
   p.unit = whole ? p.tiles : 1;
   if (whole) p.ctas = (int32_t)std::min<int64_t>(p.ctas, all_pairs);
   p.per = (int32_t)(total / p.unit / p.ctas);
@@ -1508,8 +1509,9 @@ qsa_status_t qsa_accumulate_weights(const float* weights, int64_t weights_stride
 }
 
 // Whether one CTA per request sums its pages itself, in one launch: a CTA reads about 50 GB/s, so for tables of 32,768
-// tokens (256 KB) that is 5 us, less than a second launch costs the host.  16 requests of 102,400 tokens take 22.7 us
-// this way and 8.7 us with two launches; with more requests than SMs the CTAs queue (256 of 40,000: 22.5 and 18).
+// tokens (256 KB) that is 5 us, less than a second launch costs the host (16 requests of 32,000: 16.4 us a call, 20.4 with
+// two).  On the device 16 requests of 102,400 tokens take 19.1 us this way and 9.3 us with two launches; with more
+// requests than SMs the CTAs queue (256 of 40,000: 20.1 and 17.1).
 static bool evict_in_one(int32_t R, int32_t max_pages, int32_t page_size) {
   return R <= 148 && max_pages <= 4096 && (int64_t)max_pages * page_size <= 32768;
 }
