@@ -202,6 +202,16 @@ def test_split_counts_agree():
     check(one, tuple(x[:8] for x in big))
 
 
+@pytest.mark.parametrize("Hq,H,width,rows", [(24, 2, 5000, 1), (4, 1, 2400, 2), (24, 2, 2310, 1), (8, 4, 9000, 3)])
+def test_lists_cut_into_many_pieces(Hq, H, width, rows):
+    """More pieces a row (up to 40) than the merge loads in one round, with and without weights."""
+    d = make([width + 300], [rows], Hq, H, 64, 16, width, seed=22)
+    got = gpu(d)
+    check(d, got)
+    bare = gpu(d, weights=False)
+    assert np.array_equal(got[0], bare[0]) and np.array_equal(got[1], bare[1])
+
+
 def test_another_stream_and_a_captured_replay():
     d = {k: v.to(DEV) for k, v in make([700, 31], [2, 3], 24, 2, 64, 16, 300, seed=16).items()}
     args = [d[k] for k in ("q", "kc", "vc", "ks", "vs", "table", "cu", "sl", "tok")]
