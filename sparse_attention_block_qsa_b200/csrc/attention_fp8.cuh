@@ -531,148 +531,150 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     }
     if (!ok || !gather_v(n - 1)) gone();
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 8) {
+  } else if (warp >= 8) {
+    // (one instruction for the warpgroup: its warps part only behind it)
     if constexpr (C::RESIDENT > 1) regs_shrink<REGS_REST>();
-    // ---------------------------------------------------------------- MMA issue
-    // The whole warp goes round, so that descriptors stay in uniform registers; one lane issues.
-    const uint64_t q_desc = umma_desc_sw128(smem_addr(q_s));
-    const uint64_t kv_desc = umma_desc_sw128(smem_addr(buf_s));
-    const uint64_t p_desc = desc_plain_mn(smem_addr(p_s), 128, TILE * 16);
-    int ks = 0, ko = 0;                                // next tile of either product
-    // K of tile k is item 2 k - 1 (0 for the first), V is item 2 k + 2 (2 n - 1 for the last)
-    auto k_item = [](int k) { return k == 0 ? 0 : 2 * k - 1; };
-    auto v_item = [&](int k) { return k + 1 < n ? 2 * k + 2 : 2 * n - 1; };
-    int sb = 0;                                        // score buffer of ks and its phase
-    uint32_t sp = 0;
-    int tile = tile0, nth = 0;                         // of S: tile in its pair, pairs begun
-    bool fresh = true;
-    uint64_t since = global_timer_ns();
-    uint32_t idle = 0;
-    while (ko < n) {
-      bool did = false;
-      const int ki = k_item(ks), kb = ki % BUFS, vi = v_item(ko), vb = vi % BUFS;
-      const uint32_t kp = (uint32_t)(ki / BUFS) & 1, vp = (uint32_t)(vi / BUFS) & 1;
-      if (ko < ks && __all_sync(0xffffffffu, mbar_test(p_full, (uint32_t)ko & 1) &&
-                                                 mbar_test(&kv_full[vb], vp))) {
-        fence_proxy_async_smem();                      // the cp.async writes, before the tensor core reads them
-        tc_fence_after();
-        const bool add = *add_s != 0;
-        const uint64_t vd = kv_desc + (uint32_t)(vb * (BUF_BYTES >> 4));
-        if (elect_one()) {
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_e4m3(tm_o + hf * PN, vd + hf * (HALF_BYTES >> 4) + s * (32 * 128 >> 4), p_desc + s * (32 * 16 >> 4),
-                       IDESC_O, add || s > 0);
-          umma_commit(&kv_empty[vb]);
-          umma_commit(o_full);
+    if (warp == 8) {
+      // ---------------------------------------------------------------- MMA issue
+      // The whole warp goes round, so that descriptors stay in uniform registers; one lane issues.
+      const uint64_t q_desc = umma_desc_sw128(smem_addr(q_s));
+      const uint64_t kv_desc = umma_desc_sw128(smem_addr(buf_s));
+      const uint64_t p_desc = desc_plain_mn(smem_addr(p_s), 128, TILE * 16);
+      int ks = 0, ko = 0;                                // next tile of either product
+      // K of tile k is item 2 k - 1 (0 for the first), V is item 2 k + 2 (2 n - 1 for the last)
+      auto k_item = [](int k) { return k == 0 ? 0 : 2 * k - 1; };
+      auto v_item = [&](int k) { return k + 1 < n ? 2 * k + 2 : 2 * n - 1; };
+      int sb = 0;                                        // score buffer of ks and its phase
+      uint32_t sp = 0;
+      int tile = tile0, nth = 0;                         // of S: tile in its pair, pairs begun
+      bool fresh = true;
+      uint64_t since = global_timer_ns();
+      uint32_t idle = 0;
+      while (ko < n) {
+        bool did = false;
+        const int ki = k_item(ks), kb = ki % BUFS, vi = v_item(ko), vb = vi % BUFS;
+        const uint32_t kp = (uint32_t)(ki / BUFS) & 1, vp = (uint32_t)(vi / BUFS) & 1;
+        if (ko < ks && __all_sync(0xffffffffu, mbar_test(p_full, (uint32_t)ko & 1) &&
+                                                   mbar_test(&kv_full[vb], vp))) {
+          fence_proxy_async_smem();                      // the cp.async writes, before the tensor core reads them
+          tc_fence_after();
+          const bool add = *add_s != 0;
+          const uint64_t vd = kv_desc + (uint32_t)(vb * (BUF_BYTES >> 4));
+          if (elect_one()) {
+  #pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+  #pragma unroll
+              for (int s = 0; s < 4; ++s)
+                mma_e4m3(tm_o + hf * PN, vd + hf * (HALF_BYTES >> 4) + s * (32 * 128 >> 4), p_desc + s * (32 * 16 >> 4),
+                         IDESC_O, add || s > 0);
+            umma_commit(&kv_empty[vb]);
+            umma_commit(o_full);
+          }
+          __syncwarp();
+          ++ko;
+          did = true;
         }
-        __syncwarp();
-        ++ko;
-        did = true;
+        if (ks < n && ks < ko + S_BUFS &&
+            __all_sync(0xffffffffu, mbar_test(&kv_full[kb], kp) &&
+                                        mbar_test(&s_empty[sb], sp ^ 1) &&
+                                        (!fresh || mbar_test(q_full, (uint32_t)nth & 1)))) {
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint64_t kd = kv_desc + (uint32_t)(kb * (BUF_BYTES >> 4));
+          const uint32_t d = tmem + (uint32_t)sb * QN;
+          const bool last = tile + 1 == p.tiles;
+          if (elect_one()) {
+  #pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_e4m3(d, kd + (s >> 2) * (HALF_BYTES >> 4) + (s & 3) * 2, q_desc + (s >> 2) * (Q_HALF >> 4) + (s & 3) * 2,
+                       IDESC_S, s > 0);
+            umma_commit(&kv_empty[kb]);
+            mbar_arrive(&s_full[sb]);                  // hands on what q_full published (the head factors)
+            umma_commit(&s_full[sb]);
+            if (last) umma_commit(q_empty);
+          }
+          __syncwarp();
+          fresh = last;
+          tile = last ? 0 : tile + 1;
+          nth += last ? 1 : 0;
+          ++ks;
+          if (++sb == S_BUFS) {
+            sb = 0;
+            sp ^= 1;
+          }
+          did = true;
+        }
+        if (did) {
+          idle = 0;
+        } else if ((++idle & 63u) == 0) {
+          if (idle == 64) since = global_timer_ns();
+          if (__any_sync(0xffffffffu, *abort != 0 || global_timer_ns() - since > QSA_WAIT_TIMEOUT_NS)) {
+            gone();
+            if (elect_one()) umma_commit(drained);       // what was issued still ends before TMEM is freed
+            mbar_wait(drained, 0, nullptr);
+            break;
+          }
+        }
       }
-      if (ks < n && ks < ko + S_BUFS &&
-          __all_sync(0xffffffffu, mbar_test(&kv_full[kb], kp) &&
-                                      mbar_test(&s_empty[sb], sp ^ 1) &&
-                                      (!fresh || mbar_test(q_full, (uint32_t)nth & 1)))) {
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint64_t kd = kv_desc + (uint32_t)(kb * (BUF_BYTES >> 4));
-        const uint32_t d = tmem + (uint32_t)sb * QN;
-        const bool last = tile + 1 == p.tiles;
-        if (elect_one()) {
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_e4m3(d, kd + (s >> 2) * (HALF_BYTES >> 4) + (s & 3) * 2, q_desc + (s >> 2) * (Q_HALF >> 4) + (s & 3) * 2,
-                     IDESC_S, s > 0);
-          umma_commit(&kv_empty[kb]);
-          mbar_arrive(&s_full[sb]);                  // hands on what q_full published (the head factors)
-          umma_commit(&s_full[sb]);
-          if (last) umma_commit(q_empty);
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- queries: warp w takes heads w, w + 3, ...
+      const int w = warp - 9;
+      const int pairs = (tile0 + n - 1) / p.tiles + 1;
+      for (int nth = 0; nth < pairs; ++nth) {
+        const int64_t t = (pair0 + nth) / p.Hkv;
+        const int g = pair0 + nth - (int)t * p.Hkv;
+        const uint16_t* q_row = p.q + t * p.q_st + (int64_t)g * p.group * p.q_sh + lane * 8;
+        constexpr int PER = (HG + Q_WARPS - 1) / Q_WARPS;
+        uint4 x4[PER];                                   // read before the wait; heads past the group are zero
+  #pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int h = w + Q_WARPS * i;
+          x4[i] = make_uint4(0, 0, 0, 0);
+          if (h < p.group) x4[i] = __ldg(reinterpret_cast<const uint4*>(q_row + h * p.q_sh));
         }
-        __syncwarp();
-        fresh = last;
-        tile = last ? 0 : tile + 1;
-        nth += last ? 1 : 0;
-        ++ks;
-        if (++sb == S_BUFS) {
-          sb = 0;
-          sp ^= 1;
-        }
-        did = true;
-      }
-      if (did) {
-        idle = 0;
-      } else if ((++idle & 63u) == 0) {
-        if (idle == 64) since = global_timer_ns();
-        if (__any_sync(0xffffffffu, *abort != 0 || global_timer_ns() - since > QSA_WAIT_TIMEOUT_NS)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (uint32_t)(nth & 1) ^ 1, abort))) {
           gone();
-          if (elect_one()) umma_commit(drained);       // what was issued still ends before TMEM is freed
-          mbar_wait(drained, 0, nullptr);
           break;
         }
-      }
-    }
-    __syncwarp();
-  } else if (warp > 8) {
-    if constexpr (C::RESIDENT > 1) regs_shrink<REGS_REST>();
-    // ---------------------------------------------------------------- queries: warp w takes heads w, w + 3, ...
-    const int w = warp - 9;
-    const int pairs = (tile0 + n - 1) / p.tiles + 1;
-    for (int nth = 0; nth < pairs; ++nth) {
-      const int64_t t = (pair0 + nth) / p.Hkv;
-      const int g = pair0 + nth - (int)t * p.Hkv;
-      const uint16_t* q_row = p.q + t * p.q_st + (int64_t)g * p.group * p.q_sh + lane * 8;
-      constexpr int PER = (HG + Q_WARPS - 1) / Q_WARPS;
-      uint4 x4[PER];                                   // read before the wait; heads past the group are zero
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int h = w + Q_WARPS * i;
-        x4[i] = make_uint4(0, 0, 0, 0);
-        if (h < p.group) x4[i] = __ldg(reinterpret_cast<const uint4*>(q_row + h * p.q_sh));
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (uint32_t)(nth & 1) ^ 1, abort))) {
-        gone();
-        break;
-      }
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int h = w + Q_WARPS * i;
-        if (h >= HG) break;
-        const uint32_t w4[4] = {x4[i].x, x4[i].y, x4[i].z, x4[i].w};
-        // the head's largest magnitude, as a 16-bit pattern (NaN and infinity sort above every number)
-        uint32_t top2 = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top2 = __vmaxu2(top2, w4[k] & 0x7fff7fffu);
-        const uint32_t top16 = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
-        const bool bad = top16 >= (F16 ? 0x7c00u : 0x7f80u);
-        // the power of two that brings it into [224, 448]: 448 = 1.75 * 2^8
-        const uint32_t tb = __float_as_uint(widen2<F16>(top16).x);
-        const int e = max((int)(tb >> 23) - 127 - 8 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
-        const float2 inv = both(bad ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - e) << 23));
-        float2 y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = mul2(widen2<F16>(w4[k]), inv);
-        const int un = lane >> 1;                      // 16-byte unit of the row
-#pragma unroll
-        for (int q = 0; q < QT; ++q) {
-          uint32_t code[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            code[k] = e4m3x2(y[k].x, y[k].y);
-            if (q + 1 < QT) y[k] = fma2(e4m3x2_value(code[k]), both(-16.f), mul2(y[k], both(16.f)));
+  #pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int h = w + Q_WARPS * i;
+          if (h >= HG) break;
+          const uint32_t w4[4] = {x4[i].x, x4[i].y, x4[i].z, x4[i].w};
+          // the head's largest magnitude, as a 16-bit pattern (NaN and infinity sort above every number)
+          uint32_t top2 = 0;
+  #pragma unroll
+          for (int k = 0; k < 4; ++k) top2 = __vmaxu2(top2, w4[k] & 0x7fff7fffu);
+          const uint32_t top16 = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
+          const bool bad = top16 >= (F16 ? 0x7c00u : 0x7f80u);
+          // the power of two that brings it into [224, 448]: 448 = 1.75 * 2^8
+          const uint32_t tb = __float_as_uint(widen2<F16>(top16).x);
+          const int e = max((int)(tb >> 23) - 127 - 8 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+          const float2 inv = both(bad ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - e) << 23));
+          float2 y[4];
+  #pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = mul2(widen2<F16>(w4[k]), inv);
+          const int un = lane >> 1;                      // 16-byte unit of the row
+  #pragma unroll
+          for (int q = 0; q < QT; ++q) {
+            uint32_t code[4];
+  #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              code[k] = e4m3x2(y[k].x, y[k].y);
+              if (q + 1 < QT) y[k] = fma2(e4m3x2_value(code[k]), both(-16.f), mul2(y[k], both(16.f)));
+            }
+            const int nr = q * HG + h;
+            uint8_t* dst = q_s + (un >> 3) * Q_HALF + nr * 128 + (((un & 7) ^ (nr & 7)) << 4) + (lane & 1) * 8;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
           }
-          const int nr = q * HG + h;
-          uint8_t* dst = q_s + (un >> 3) * Q_HALF + nr * 128 + (((un & 7) ^ (nr & 7)) << 4) + (lane & 1) * 8;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+          if (lane == 0)
+            qc_s[(nth % QC_SLOTS) * HG + h] =
+                h < p.group ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : 0.f;
         }
-        if (lane == 0)
-          qc_s[(nth % QC_SLOTS) * HG + h] =
-              h < p.group ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : 0.f;
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
       }
-      fence_proxy_async_smem();
-      mbar_arrive(q_full);
     }
   } else {
     // ---------------------------------------------------------------- softmax
