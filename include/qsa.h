@@ -446,9 +446,12 @@ size_t qsa_mqa_paged_batch_workspace_size(int32_t R, int32_t num_decodes, int32_
  *              one pool, are all strides.
  *   k_scale,   fp32 [num_pages, page_size / block_tokens, Hkv]: page and
  *   v_scale    block strides in elements, unit head stride; >= 2^-126 and
- *              finite for every block that holds a token.  A k_scale of 0
- *              (memory zeroed once) marks a block and head that holds none:
- *              attention does not see its tokens, whatever their codes are.
+ *              finite for every block that holds a token, the v_scales of
+ *              the tokens that one row sees within 2^190 of each other (those
+ *              that qsa_kv_append_fp8 writes lie in 2^-64 .. 2^120).  A
+ *              k_scale of 0 (memory zeroed once) marks a block and head that
+ *              holds none: attention does not see its tokens, whatever their
+ *              codes are.
  *   block_tokens  1 .. page_size, dividing page_size (any page_size >= 1).
  * The pages' K/V cache is 16-bit; this one halves its memory and traffic.
  * Requests, rows and page tables are those of qsa_sparse_attention: row i of
@@ -507,7 +510,8 @@ qsa_status_t qsa_kv_append_fp8_f16(const void* k, int64_t k_stride_t, int64_t k_
  * Codes enter the tensor cores as they are; queries and probabilities are
  * split into E4M3 terms (a 16-bit query element exactly, down to 2^-22 of its
  * head's largest; a probability times its v_scale to 2^-16 relative, down to
- * 2^-22 of the largest), all sums are fp32.
+ * 2^-22 of the head's largest such product), all sums are fp32.  A large
+ * v_scale at a token that gets no attention takes nothing from the others.
  *   weights    fp32 [T, width], row stride weights_stride (>= width), or
  *              NULL: weights[t, e] = sum over the Hq query heads of entry e's
  *              softmax probability, 0 for entries that the row does not see.

@@ -18,11 +18,11 @@
 //  * The output is O^T = V^T P: the V rows stay [entry][feature] in shared
 //    memory and are read as an M-major operand (M = 128 features, two
 //    halves), P as an N-major one, so that a thread writes its heads' codes in
-//    16-byte stores.  P (times v_scale_j over a reference v_scale) is split into
-//    four terms the same way: 2^-16 relative, 2^-22 of the reference, well below
-//    the 16-bit output's rounding.  Four, not three, because the reference below
-//    may lag by 2^6 and 7; the N columns of 8 or 12 heads, a multiple of 16, have
-//    room for them anyway.
+//    16-byte stores.  The products p_hj v_scale_j are split into four terms the
+//    same way: 2^-16 relative, 2^-22 of the head's largest product, well below the
+//    16-bit output's rounding.  Four, not three, because the reference below may
+//    lag by 2^8.75; the N columns of 8 or 12 heads, a multiple of 16, have room for
+//    them anyway.
 //  * Sums over entries are fp32: of the probabilities in registers, of the
 //    output in TMEM and, when the reference moves, in registers.
 //
@@ -38,10 +38,14 @@
 //  * warp 8 issues the MMAs, whichever product has its operands: S runs up to
 //    S_BUFS tiles ahead of the softmax;
 //  * warps 9-11 split each new row's queries;
-//  * warps 0-3 run the softmax (thread = entry, then feature).  Scores are taken
-//    relative to a reference maximum that moves only when a tile exceeds it by
-//    2^6 (or its v_scale by a factor of 7): until then a tile needs no reduction,
-//    only a vote, and its output product adds up in TMEM.
+//  * warps 0-3 run the softmax (thread = entry, then feature).  What is split into
+//    terms is 2^(s + log2 v_scale - R), R a reference by head for the products: the
+//    v_scales may differ by any factor, and a large one where nothing attends does
+//    not push the others' products below what the terms hold.  R moves only when a
+//    tile exceeds it by more than the terms have room for: until then a tile needs
+//    no reduction, only a vote, and its output product adds up in TMEM.  The sum of
+//    the probabilities takes the same exponentials over v_scale.  (Exponentials of
+//    its own, 2^(s - M) with a second reference: 234 us in place of 210 for 1,024 rows.)
 //
 // Measured on B200 (24 / 2 heads, 2,051 entries a row): 16 requests x 4 rows
 // 25.4 us with the merge (108 MB of distinct rows, 110 MB of DRAM reads; 16.5 us at
@@ -71,9 +75,16 @@ constexpr int THREADS = SOFT + PROD + 128;   // the last warpgroup: MMA issue, q
 // warpgroups then share them out (the same sum of 240).
 constexpr int REGS_LAUNCH = 80, REGS_SOFT = 152, REGS_PROD = 48, REGS_REST = 40;
 static_assert(REGS_SOFT + REGS_PROD + REGS_REST <= 3 * REGS_LAUNCH, "setmaxnreg would wait for ever");
-// A probability is at most 2^REF_SLACK times the reference and v_scale at most
-// V_SLACK times its own: together 448, E4M3's largest value.
-constexpr float REF_SLACK = 6.f, V_SLACK = 7.f;
+// log2 of a product p v_scale relative to its reference: the largest is brought to [0, 1) when the references move, and
+// they move again above PROD_MOST (2^8.75 = 430; E4M3's largest value is 448).  The terms end at 2^-22.  (References 2^4
+// lower, for products held to 2^-26 of the largest, move more often: 1,024 rows 248 us in place of 229 then.)
+constexpr float PROD_MOST = 8.75f;
+// Probabilities are added up as 2^(s - R + U), U = log2 of the largest v_scale in the tiles that moved the references,
+// minus V_DROP.  The entry that R is from adds at least 2^-V_DROP, and one whose v_scale is 2^-d of that largest at
+// most 2^(PROD_MOST + d - V_DROP): for d up to 190 and 2^20 entries both are fp32 numbers.  A product below 2^-126 is 0,
+// which stands for a probability below 2^(d - 126) of the sum: from d = V_DROP on, exponentials of their own.
+constexpr float V_DROP = 90.f;
+constexpr float V_ZERO = -150.f;       // stands for log2 of a v_scale of 0: nothing that a 16-bit output holds
 constexpr int MAX_GROUP = 16;          // query heads per KV head
 constexpr int PT = 4;                  // E4M3 terms of a probability
 constexpr int BUFS = 3;
@@ -148,7 +159,8 @@ struct Params {
   int32_t unit, per, more;    // a unit is one tile, or the tiles of a pair (no run then ends inside one)
   float scale_log2;
   float* part_o;              // [2 ctas, group, 256] unnormalised outputs of pairs cut by a run's ends
-  float* part_ml;             // [2 ctas, group, 2] maximum (log2 units), sum
+  float* part_ml;             // [2 ctas, group, 2] reference score (log2 units), sum
+  float* part_d;              // [2 ctas, group] the outputs are 2^d times what they are relative to the reference score
   float* part_s;              // [T, Hq, width] scores (log2 units), or null
   float* lse2;                // [T, Hq] log2 of the sum of 2^s (of pairs that no run cuts), or null
   const float* gate;
@@ -236,10 +248,24 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
   for (int i = 0; i < N; i += 8) tmem_ld8(taddr + i, v + i);
 }
 
+__device__ __forceinline__ float log2_fast(float x) {   // 2 ulp (2^-22 for 0.5 to 2); log2(0) = -infinity
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 2^-inf = 0
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// 2^n, n whole and between -126 and 127 (further out: the nearest of them)
+__device__ __forceinline__ float power_of_two(float n) {
+  return __int_as_float(((int)fminf(fmaxf(n, -126.f), 127.f) + 127) << 23);
 }
 
 __device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
@@ -684,9 +710,11 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
     if constexpr (!C::RING) f.start(p, pair0, tile0, n, tid, lane);
     // heads 2 i, 2 i + 1: sums over this thread's entries; features tid and 128 + tid
     float2 l_run[HG / 2], o0[HG / 2], o1[HG / 2];
-    float2 nref[HG / 2];                               // the references, negated; same in every thread
-    float vref = 0.f, vinv = 0.f;
-    bool set = false;                                  // mref holds maxima: a tile had a visible entry
+    // References, same in every thread and whole numbers, so that moving them rounds nothing however often they move:
+    // of the products, by head (negated), and U.
+    float2 nref[HG / 2];
+    float vsum = 0.f;
+    bool set = false;                                  // the references hold maxima: a tile had a visible entry
     bool add = false;                                  // TMEM holds output of this pair that o0, o1 lack
     int pair = pair0, tile = tile0, nth = 0;
     int sb = 0;                                        // score buffer and its phase
@@ -710,7 +738,6 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       tc_fence_after();
     };
     auto take_output = [&]() {                         // o += what TMEM holds
-      const float2 unit = both(vref);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         float d[(C::PCOLS + 7) / 8 * 8];
@@ -723,14 +750,15 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           x = fma2(make_float2(d[HG + 2 * i], d[HG + 2 * i + 1]), both(1.f / 16.f), x);
           x = fma2(make_float2(d[2 * HG + 2 * i], d[2 * HG + 2 * i + 1]), both(1.f / 256.f), x);
           x = fma2(make_float2(d[3 * HG + 2 * i], d[3 * HG + 2 * i + 1]), both(1.f / 4096.f), x);
-          o[i] = fma2(x, unit, o[i]);
+          o[i] = add2(o[i], x);
         }
       }
     };
     for (int k = 0; k < n; ++k) {
       bool seen;
       float ks = ks_nx, vs = vs_nx;
-      float2 x[HG / 2];                                // scores, then relative to mref, then probabilities
+      float lvs;                                       // log2 v_scale, to 2 ulp
+      float2 x[HG / 2];                                // log2 of the products, relative to their references
       {
         if (!mbar_wait(&s_full[sb], sp, abort)) gone();
         tc_fence_after();
@@ -741,11 +769,10 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         }
         // unseen entries come with scales of 0, and a k_scale of 0 marks a block that holds nothing
         seen = ks != 0.f;
-        if (!seen) vs = 0.f;
+        lvs = seen ? max_or_nan(log2_fast(vs), V_ZERO) : 0.f;
         if (fresh) {
 #pragma unroll
           for (int i = 0; i < HG / 2; ++i) nref[i] = l_run[i] = o0[i] = o1[i] = make_float2(0.f, 0.f);
-          vref = vinv = 0.f;
           add = set = false;
         }
         const float2* qc = reinterpret_cast<const float2*>(qc_s + (nth % QC_SLOTS) * HG);
@@ -763,7 +790,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           x[i] = fma2(make_float2(d[HG + 2 * i], d[HG + 2 * i + 1]), both(1.f / 16.f), make_float2(d[2 * i], d[2 * i + 1]));
           if (QT > 2)
             x[i] = fma2(make_float2(d[(QT - 1) * HG + 2 * i], d[(QT - 1) * HG + 2 * i + 1]), both(1.f / 256.f), x[i]);
-          x[i] = fma2(x[i], mul2(qc[i], both(ks)), nref[i]);
+          x[i] = fma2(x[i], mul2(qc[i], both(ks)), add2(nref[i], both(lvs)));
         }
         if (!__all_sync(0xffffffffu, seen)) {
 #pragma unroll
@@ -776,8 +803,11 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         if (e < p.width) {
           float* dst = p.part_s + (int64_t)pair * p.group * p.width + e;
 #pragma unroll
-          for (int h = 0; h < HG; ++h)
-            if (h < p.group) dst[(int64_t)h * p.width] = h & 1 ? x[h / 2].y - nref[h / 2].y : x[h / 2].x - nref[h / 2].x;
+          for (int i = 0; i < HG / 2; ++i) {
+            const float2 at = add2(nref[i], both(lvs));
+            if (2 * i < p.group) dst[(int64_t)(2 * i) * p.width] = x[i].x - at.x;
+            if (2 * i + 1 < p.group) dst[(int64_t)(2 * i + 1) * p.width] = x[i].y - at.y;
+          }
         }
       }
       float over = -INFINITY;
@@ -785,15 +815,16 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       for (int i = 0; i < HG / 2; ++i) {
         over = fmaxf(over, fmaxf(x[i].x, x[i].y));
       }
-      if (barrier_any(1, SOFT, !set || over > REF_SLACK || vs > V_SLACK * vref)) {
+      if (barrier_any(1, SOFT, !set || over > PROD_MOST)) {
         // ---- new references: the tile's maxima where they are larger
+        auto maximum = [&](const float* at) { return floorf(fmaxf(fmaxf(at[0], at[17]), fmaxf(at[34], at[51]))); };
         float mine = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HG; ++h) {
           const float wm = warp_max(h & 1 ? x[h / 2].y - nref[h / 2].y : x[h / 2].x - nref[h / 2].x);
           if (lane == h) mine = wm;
         }
-        const float vm = warp_max(vs);
+        const float vm = warp_max(seen ? lvs : -INFINITY);
         if (lane == 16) mine = vm;
         if (lane <= 16) red_s[warp * 17 + lane] = mine;
         named_barrier_sync(2, SOFT);
@@ -802,35 +833,44 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           take_output();
           add = false;
         }
-        vref = fmaxf(vref, fmaxf(fmaxf(red_s[16], red_s[33]), fmaxf(red_s[50], red_s[67])));
-        vinv = vref > 0.f ? 1.f / vref : 0.f;
-        bool any = false;
+        const bool was_set = set;
+        const float was = vsum, top = maximum(red_s + 16) - V_DROP;
+        if (top > -INFINITY) {                         // something is visible
+          vsum = set ? fmaxf(vsum, top) : top;
+          set = true;
+        }
 #pragma unroll
         for (int i = 0; i < HG / 2; ++i) {
           float a[2], nr[2] = {nref[i].x, nref[i].y};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int h = 2 * i + e;
-            float m = fmaxf(fmaxf(red_s[h], red_s[17 + h]), fmaxf(red_s[34 + h], red_s[51 + h]));
-            any = any || m > -INFINITY;
-            if (set) m = fmaxf(m, -nr[e]);
-            if (!(m > -INFINITY)) m = 0.f;             // nothing visible yet (or only NaN)
-            a[e] = -nr[e] - m;
-            nr[e] = -m;
+            float r = maximum(red_s + 2 * i + e);
+            if (was_set) r = fmaxf(r, -nr[e]);
+            if (!(r > -INFINITY)) r = 0.f;             // nothing visible yet (or only NaN)
+            a[e] = -nr[e] - r;
+            nr[e] = -r;
           }
           nref[i] = make_float2(nr[0], nr[1]);
           x[i] = add2(x[i], make_float2(a[0], a[1]));
-          const float2 alpha = set ? make_float2(exp2_fast(a[0]), exp2_fast(a[1])) : both(1.f);
-          l_run[i] = mul2(l_run[i], alpha);
-          o0[i] = mul2(o0[i], alpha);
-          o1[i] = mul2(o1[i], alpha);
+          if (was_set) {                               // (else there is nothing to rescale)
+            const float2 alpha = make_float2(exp2_fast(a[0]), exp2_fast(a[1]));
+            l_run[i] = mul2(l_run[i], make_float2(exp2_fast(a[0] + (vsum - was)), exp2_fast(a[1] + (vsum - was))));
+            o0[i] = mul2(o0[i], alpha);
+            o1[i] = mul2(o1[i], alpha);
+          }
         }
-        set = set || any;
         named_barrier_sync(2, SOFT);                   // red_s may be written again
       }
+      float per_v = vsum - lvs;
+      if (per_v > 0.f && seen) {                       // the v_scale is 2^-V_DROP of the largest: p by itself
+#pragma unroll
+        for (int i = 0; i < HG / 2; ++i)
+          l_run[i] = add2(l_run[i], make_float2(exp2_fast(x[i].x + per_v), exp2_fast(x[i].y + per_v)));
+        per_v = -INFINITY;
+      }
+      per_v = exp2_fast(per_v);                        // (a number for unseen entries too)
       if constexpr (!C::RING) scales();                // of tile k + 1
-      // ---- P times v_scale / vref as four E4M3 terms
-      const float2 vn = both(vs * vinv);
+      // ---- P times v_scale as four E4M3 terms
       uint32_t w4[PN / 4];
 #pragma unroll
       for (int i = 0; i < PN / 4; ++i) w4[i] = 0;
@@ -839,9 +879,8 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
         float2 y[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float2 pr = make_float2(exp2_fast(x[2 * c + e].x), exp2_fast(x[2 * c + e].y));
-          l_run[2 * c + e] = add2(l_run[2 * c + e], pr);
-          y[e] = mul2(pr, vn);
+          y[e] = make_float2(exp2_fast(x[2 * c + e].x), exp2_fast(x[2 * c + e].y));
+          l_run[2 * c + e] = fma2(y[e], both(per_v), l_run[2 * c + e]);
         }
 #pragma unroll
         for (int q = 0; q < PT; ++q) {
@@ -868,21 +907,26 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
       if (fresh || k + 1 == n) {
         // ---- end of the pair or of the run: output, or the piece for the merge
         const bool whole = fresh && k + 1 >= p.tiles;
-        float mine = 0.f, mref_lane = 0.f;             // of head `lane`
+        const int at = lane & 15;
+        float mine = 0.f, ref = 0.f;                   // of head `at`
 #pragma unroll
         for (int h = 0; h < HG; ++h) {
           float l = h & 1 ? l_run[h / 2].y : l_run[h / 2].x;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-          if (lane == h) {
+          if (at == h) {
             mine = l;
-            mref_lane = h & 1 ? -nref[h / 2].y : -nref[h / 2].x;
+            ref = h & 1 ? -nref[h / 2].y : -nref[h / 2].x;
           }
         }
         if (lane < 16) red_s[warp * 17 + lane] = mine;
         named_barrier_sync(2, SOFT);
-        const int at = lane & 15;
-        const float l = red_s[at] + red_s[17 + at] + red_s[34 + at] + red_s[51 + at];
+        float l = red_s[at] + red_s[17 + at] + red_s[34 + at] + red_s[51 + at];
+        // The sum as a number in [1, 2) and its reference score, so that pieces with other references compare; the
+        // outputs are 2^more times what they are relative to that.
+        const float e = l > 0.f && l < INFINITY ? (float)((int)(__float_as_uint(l) >> 23) - 127) : 0.f;
+        const float mref = ref - vsum + e, more = e - vsum;
+        l *= power_of_two(-e);
         named_barrier_sync(2, SOFT);
         const int64_t t = pair / p.Hkv;
         const int g = pair - (int)t * p.Hkv;
@@ -892,17 +936,20 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
           float mul = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays NaN
           const int64_t hq = t * p.Hq + (int64_t)g * p.group;
           if (p.gate && at < p.group) mul *= 1.f / (1.f + expf(-p.gate[hq + at]));
+          const float half = floorf(more * 0.5f);      // 2^-more in two factors: it may lie outside fp32's range
+          const float unit = power_of_two(-half);
+          mul *= power_of_two(half - more);
           uint16_t* out = p.out + t * p.out_st + (int64_t)g * p.group * D + tid;
 #pragma unroll
           for (int h = 0; h < HG; ++h) {
-            const float m = __shfl_sync(0xffffffffu, mul, h);
+            const float m = __shfl_sync(0xffffffffu, mul, h), u = __shfl_sync(0xffffffffu, unit, h);
             if (h < p.group) {
-              out[h * D] = narrow<F16>((h & 1 ? o0[h / 2].y : o0[h / 2].x) * m);
-              out[h * D + 128] = narrow<F16>((h & 1 ? o1[h / 2].y : o1[h / 2].x) * m);
+              out[h * D] = narrow<F16>((h & 1 ? o0[h / 2].y : o0[h / 2].x) * u * m);
+              out[h * D + 128] = narrow<F16>((h & 1 ? o1[h / 2].y : o1[h / 2].x) * u * m);
             }
           }
           if (warp == 0 && lane < p.group) {
-            const float l2 = l == 0.f ? -INFINITY : mref_lane + log2f(l);
+            const float l2 = l == 0.f ? -INFINITY : mref + log2f(l);
             if (p.lse) p.lse[hq + lane] = l2 * 0.69314718055994531f;
             if (p.lse2) p.lse2[hq + lane] = l2;
           }
@@ -917,8 +964,9 @@ __global__ void __launch_bounds__(THREADS, (Cfg<F16, HG>::RESIDENT)) attn_fp8_ke
               po[h * D + 128] = h & 1 ? o1[h / 2].y : o1[h / 2].x;
             }
           if (warp == 0 && lane < p.group) {
-            p.part_ml[(slot * p.group + lane) * 2] = l == 0.f ? -INFINITY : mref_lane;
+            p.part_ml[(slot * p.group + lane) * 2] = l == 0.f ? -INFINITY : mref;
             p.part_ml[(slot * p.group + lane) * 2 + 1] = l;
+            p.part_d[slot * p.group + lane] = more;
           }
         }
       }
@@ -1025,31 +1073,40 @@ __global__ void __launch_bounds__(MERGE_THREADS) finish_fp8_kernel(const Params 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // every CTA: the grid must not end before the attention does
   if (!mine || hh >= p.group) return;
   // (plain loads: the pieces are written while this grid is already launched)
-  float M = -INFINITY, sum = 0.f;
+  // Sums relative to the largest reference score M so far, outputs 2^P times those: P as large as every piece allows.
+  float M = -INFINITY, P = 0.f, sum = 0.f;
   float2 acc = make_float2(0.f, 0.f);
   for (int i0 = 0; i0 < pieces; i0 += BATCH) {
     float2 ml[BATCH], o[BATCH];
+    float pd[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       ml[i] = make_float2(-INFINITY, 0.f);
       o[i] = make_float2(0.f, 0.f);
+      pd[i] = 0.f;
       if (i0 + i < pieces) {
         ml[i] = *reinterpret_cast<const float2*>(p.part_ml + slot(i0 + i) * 2);
+        pd[i] = p.part_d[slot(i0 + i)];
         o[i] = reinterpret_cast<const float2*>(p.part_o + slot(i0 + i) * D)[f2];
       }
     }
     float m = M;
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) m = fmaxf(m, ml[i].x);
-    const float mr = m == -INFINITY ? 0.f : m;
-    const float a = exp2f(M - mr);                     // 0 while nothing was visible
+    if (m == -INFINITY) continue;                      // nothing visible so far
+    const float a = M - m;                             // -infinity until something is
+    float d = P - a;                                   // (infinity for pieces without anything visible)
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) d = fminf(d, pd[i] + (m - ml[i].x));
+    const float e = exp2_fast(a + (d - P));            // at most 1, 0 in the first round
+    sum *= exp2_fast(a);
+    acc = make_float2(acc.x * e, acc.y * e);
     M = m;
-    sum *= a;
-    acc = make_float2(acc.x * a, acc.y * a);
+    P = d;
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      const float w = exp2f(ml[i].x - mr);
-      sum = fmaf(w, ml[i].y, sum);
+      const float b = ml[i].x - m, w = exp2_fast(b + (d - pd[i]));
+      sum = fmaf(exp2_fast(b), ml[i].y, sum);
       acc.x = fmaf(w, o[i].x, acc.x);
       acc.y = fmaf(w, o[i].y, acc.y);
     }
@@ -1058,8 +1115,11 @@ __global__ void __launch_bounds__(MERGE_THREADS) finish_fp8_kernel(const Params 
   const int h = (pair - (int)t * p.Hkv) * p.group + hh;
   float mul = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // a NaN sum stays NaN
   if (p.gate) mul *= 1.f / (1.f + expf(-p.gate[t * p.Hq + h]));
+  const float half = floorf(0.5f * P);                 // 2^-P in two factors, as above
+  const float unit = power_of_two(-half);
+  mul *= power_of_two(half - P);
   reinterpret_cast<uint32_t*>(p.out + t * p.out_st + (int64_t)h * D)[f2] =
-      (uint32_t)narrow<F16>(acc.x * mul) | ((uint32_t)narrow<F16>(acc.y * mul) << 16);
+      (uint32_t)narrow<F16>(acc.x * unit * mul) | ((uint32_t)narrow<F16>(acc.y * unit * mul) << 16);
   if (f2 == 0) {
     const float l2 = sum == 0.f ? -INFINITY : M + log2f(sum);
     if (p.lse) p.lse[t * p.Hq + h] = l2 * 0.69314718055994531f;

@@ -457,7 +457,7 @@ int64_t attn8_tiles(int32_t width) { return std::max<int64_t>(1, ((int64_t)width
 
 // Workspace of the 8-bit cache's attention (bytes from its start).
 struct Attn8Layout {
-  size_t ml, lse2, s, total;
+  size_t ml, d, lse2, s, total;
 };
 
 Attn8Layout attn8_layout(int64_t T, int32_t Hq, int32_t Hkv, int32_t width, bool weights) {
@@ -465,7 +465,8 @@ Attn8Layout attn8_layout(int64_t T, int32_t Hq, int32_t Hkv, int32_t width, bool
   const size_t pieces = 2 * (size_t)std::min(kAttn8Runs, T * Hkv * attn8_tiles(width)) * (size_t)(Hq / Hkv);
   Attn8Layout w;
   w.ml = pieces * qsa::attn8::D * sizeof(float);
-  w.lse2 = w.ml + pieces * 2 * sizeof(float);
+  w.d = w.ml + pieces * 2 * sizeof(float);
+  w.lse2 = w.d + pieces * sizeof(float);
   w.s = w.lse2 + (weights ? heads * sizeof(float) : 0);
   w.total = w.s + (weights ? heads * (size_t)width * sizeof(float) : 0);
   return w;
@@ -1413,6 +1414,7 @@ static qsa_status_t attention_fp8_common(
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.part_d = reinterpret_cast<float*>(ws + w.d);
   p.lse2 = want_w ? reinterpret_cast<float*>(ws + w.lse2) : nullptr;
   p.part_s = want_w ? reinterpret_cast<float*>(ws + w.s) : nullptr;
   p.gate = gate;
