@@ -551,7 +551,7 @@ qsa_status_t qsa_sparse_attention_fp8_f16(const void* q, int64_t q_stride_t, int
                                           int64_t weights_stride, void* workspace, size_t workspace_bytes,
                                           void* stream);
 
-/* 0 when there is nothing to compute (T, Hq, Hkv or width <= 0). */
+/* 0 when there is nothing to compute (T, Hq, Hkv or width <= 0): such calls take no workspace (NULL will do). */
 size_t qsa_sparse_attention_fp8_workspace_size(int64_t T, int32_t Hq, int32_t Hkv, int32_t width, int32_t weights);
 
 /*

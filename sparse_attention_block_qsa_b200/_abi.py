@@ -649,7 +649,7 @@ def sparse_attention_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
             raise ValueError("lse must be contiguous fp32 [T, Hq]")
     need = 0
     if workspace is None:
-        need = sparse_attention_fp8_workspace_size(T, Hq, Hkv, width if width > 0 else 1, weights is not None)
+        need = sparse_attention_fp8_workspace_size(T, Hq, Hkv, width, weights is not None)
     wp, nbytes, workspace = _workspace(workspace, need, stream, dev)
     _call(dev, "qsa_sparse_attention_fp8_f16" if dt == torch.float16 else "qsa_sparse_attention_fp8",
           q.data_ptr(), qs[0], qs[1], Hq, *cache, *tables, token_idx.data_ptr(), ts[0], width, T, gate_p, scale,

@@ -1347,9 +1347,11 @@ static qsa_status_t attention_fp8_common(
   const int32_t width1 = width > 0 ? width : 1;
   const bool want_w = weights != nullptr && width > 0;
   const Attn8Layout w = attn8_layout(T, Hq, Hkv, width1, weights != nullptr);
-  if (!workspace || workspace_bytes < w.total)
-    return fail(QSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace_bytes, w.total);
-  if (!aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if (width > 0) {                                     // (no list: one empty tile a pair, which no run cuts)
+    if (!workspace || workspace_bytes < w.total)
+      return fail(QSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace_bytes, w.total);
+    if (!aligned(workspace, 16)) return fail(QSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  }
   // The cache as one matrix of 256-byte rows, `pitch` bytes apart: every (page, token, head) row is one of them.
   const int64_t page_stride = num_pages > 1 ? kv_page_stride : 0, row_stride = page_size > 1 ? kv_row_stride : 0,
                 head_stride = Hkv > 1 ? kv_head_stride : 0;
