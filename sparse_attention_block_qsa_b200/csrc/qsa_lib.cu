@@ -160,19 +160,6 @@ qsa_status_t device_info(int* sms) {
         {reinterpret_cast<const void*>(qsa::topk::topk_list_kernel),
          qsa::topk::TP_LIST_WARPS * qsa::topk::tp_list_warp_bytes(qsa::topk::MAX_W)},
     };
-    // These kernels share their launch registers out by setmaxnreg: fewer than they count on would never do.
-    for (const void* fn : {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>),
-                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 12>),
-                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 16>),
-                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>),
-                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>)}) {
-      cudaFuncAttributes a = {};
-      e = cudaFuncGetAttributes(&a, fn);
-      if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
-      if (a.numRegs < qsa::attn8::REGS_LAUNCH)
-        return fail(QSA_ERR_UNSUPPORTED, "attention over the 8-bit cache was built with %d registers a thread; %d needed",
-                    a.numRegs, qsa::attn8::REGS_LAUNCH);
-    }
     for (auto& k : kernels) {
       e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.bytes);
       if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -454,6 +441,31 @@ void attn_splits(int64_t T, int32_t Hkv, int32_t width, int32_t* splits, int32_t
 constexpr int64_t kAttn8Runs = 296;
 
 int64_t attn8_tiles(int32_t width) { return std::max<int64_t>(1, ((int64_t)width + qsa::attn8::TILE - 1) / qsa::attn8::TILE); }
+
+// These kernels share their launch registers out by setmaxnreg: launched with fewer than they count on, they would wait
+// for ever.  Only the call that launches them refuses such a build.
+qsa_status_t attn8_registers() {
+  static std::atomic<int> fewest{0};                   // a thread's, of all instances; 0: not asked for yet
+  int n = fewest.load(std::memory_order_relaxed);
+  if (n == 0) {
+    n = INT32_MAX;
+    for (const void* fn : {reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 8>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 12>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<false, 16>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 8>),
+                           reinterpret_cast<const void*>(qsa::attn8::attn_fp8_kernel<true, 12>)}) {
+      cudaFuncAttributes a = {};
+      const cudaError_t e = cudaFuncGetAttributes(&a, fn);
+      if (e != cudaSuccess) return fail(QSA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+      n = std::min(n, a.numRegs);
+    }
+    fewest.store(n, std::memory_order_relaxed);
+  }
+  if (n < qsa::attn8::REGS_LAUNCH)
+    return fail(QSA_ERR_UNSUPPORTED, "attention over the 8-bit cache was built with %d registers a thread; %d needed", n,
+                qsa::attn8::REGS_LAUNCH);
+  return QSA_OK;
+}
 
 // Workspace of the 8-bit cache's attention (bytes from its start).
 struct Attn8Layout {
@@ -1366,6 +1378,8 @@ static qsa_status_t attention_fp8_common(
                 "2^31 - 2 supported", (long long)rows, (long long)pitch);
   int sms = 0;
   st = device_info(&sms);
+  if (st != QSA_OK) return st;
+  st = attn8_registers();
   if (st != QSA_OK) return st;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   Params p;

@@ -21,3 +21,14 @@ def test_each_warpgroup_has_one_register_instruction():
     # and the branch in front of each is taken by whole warpgroups
     branch = re.findall(r"(?:if \(([^{}]*)\)|else) \{\s*if constexpr \(C::RESIDENT > 1\) regs_(?:shrink|grow)<(\w+)>", kernel)
     assert branch == [("warp >= 4 && warp < 8", "REGS_PROD"), ("warp >= 8", "REGS_REST"), ("", "REGS_SOFT")], branch
+
+
+def test_a_build_detail_of_one_kernel_refuses_its_own_call_only():
+    """How many registers the 8-bit attention was built with is checked by that call, not by what every call shares."""
+    lib = source("qsa_lib.cu")
+    body = re.search(r"qsa_status_t device_info\(int\* sms\) \{\n(.*?)\n\}\n", lib, re.S).group(1)
+    assert "cudaFuncSetAttribute" in body            # (this is the function meant)
+    assert "numRegs" not in body and "attn8_registers" not in body
+    check = re.search(r"qsa_status_t attn8_registers\(\) \{\n(.*?)\n\}\n", lib, re.S).group(1)
+    assert "numRegs" in check and "REGS_LAUNCH" in check
+    assert len(re.findall(r"= attn8_registers\(\);", lib.split("static qsa_status_t attention_fp8_common(")[1])) == 1
