@@ -480,6 +480,9 @@ size_t qsa_mqa_paged_batch_workspace_size(int32_t R, int32_t num_decodes, int32_
  *   k, v       bf16 [T, Hkv, 256], each with its own row and head strides
  *              (positive multiples of 8 elements); 16-byte aligned; must not
  *              overlap the caches.
+ *   Strides of the caches and of the scales must nest, each at least the
+ *   extent of the dimensions with smaller strides, and K and V must not share
+ *   anything: QSA_ERR_INVALID_ARG otherwise (blocks are written concurrently).
  *   token_weight  int64 [num_pages, page_size] contiguous, or NULL: set to 0
  *              for the tokens written (see qsa_accumulate_weights).
  * One launch.

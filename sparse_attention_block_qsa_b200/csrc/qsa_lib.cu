@@ -505,10 +505,42 @@ qsa_status_t check_kv8(const void* k_cache, const void* v_cache, const float* k_
   if (num_pages > 1 && kv_page_stride < D) return fail(QSA_ERR_INVALID_ARG, "kv_page_stride below 256 bytes");
   const int32_t blocks = page_size / block_tokens;
   if (blocks > 1 && sc_block_stride < Hkv) return fail(QSA_ERR_INVALID_ARG, "scale block stride below Hkv");
-  if (num_pages > 1 && sc_page_stride < (blocks > 1 ? 1 : Hkv))
-    return fail(QSA_ERR_INVALID_ARG, "scale page stride too small");
+  if (num_pages > 1 && sc_page_stride < Hkv) return fail(QSA_ERR_INVALID_ARG, "scale page stride below Hkv");
   return QSA_OK;
 }
+
+// A set of places sum(i_k * stride_k), 0 <= i_k < count_k, each `width` wide.
+struct Places {
+  int64_t count[3], stride[3], width;
+
+  // Sorts the dimensions, the widest stride first; whether they nest, each stride at least the extent of what lies
+  // inside.  No two places then share anything.
+  bool nest() {
+    for (int a = 0; a < 3; ++a)
+      for (int b = a + 1; b < 3; ++b)
+        if (count[a] < 2 || (count[b] > 1 && stride[b] > stride[a])) {
+          std::swap(count[a], count[b]);
+          std::swap(stride[a], stride[b]);
+        }
+    int64_t extent = width;
+    for (int k = 2; k >= 0; --k) {
+      if (count[k] < 2) continue;
+      if (stride[k] < extent) return false;
+      extent += (count[k] - 1) * stride[k];
+    }
+    return true;
+  }
+  // Whether a place of this set and one of the same set moved by `by` share anything (strides that nest).  What lies
+  // inside a dimension moves a place by less than its stride, so that two steps of it can bring the places together.
+  bool meets(int64_t by, int k = 0) const {
+    if (k == 3) return by < width && by > -width;
+    if (count[k] < 2) return meets(by, k + 1);
+    int64_t steps = -(by / stride[k]) - (by % stride[k] > 0 ? 1 : 0);   // floor(-by / stride)
+    for (int i = 0; i < 2; ++i, ++steps)
+      if (steps > -count[k] && steps < count[k] && meets(by + steps * stride[k], k + 1)) return true;
+    return false;
+  }
+};
 
 // Sizes that every call on an 8-bit K/V cache checks first.
 qsa_status_t check_kv8_sizes(int64_t T, int32_t R, int64_t num_pages, int32_t page_size, int32_t block_tokens,
@@ -1231,7 +1263,13 @@ static qsa_status_t append_common(const void* k, int64_t k_stride_t, int64_t k_s
                             page_size > 1 ? kv_row_stride : 0, Hkv, Hkv > 1 ? kv_head_stride : 0, D);
       if (overlaps(rc, in[0]) || overlaps(rc, in[1])) return fail(QSA_ERR_INVALID_ARG, "a cache overlaps k or v");
     }
-    if (k_cache == v_cache || k_scale == v_scale)
+    // Blocks are written concurrently: no two may share anything.
+    Places rows = {{num_pages, page_size, Hkv}, {kv_page_stride, kv_row_stride, kv_head_stride}, D};
+    Places scales = {{num_pages, page_size / block_tokens, 1}, {sc_page_stride, sc_block_stride, 0}, Hkv};
+    if (!rows.nest() || !scales.nest())
+      return fail(QSA_ERR_INVALID_ARG, "rows or scales of the cache overlap each other: every stride must be at least the "
+                  "extent of the dimensions with smaller ones");
+    if (rows.meets(static_cast<const char*>(v_cache) - static_cast<const char*>(k_cache)) || scales.meets(v_scale - k_scale))
       return fail(QSA_ERR_INVALID_ARG, "K and V need caches and scales of their own");
   }
   const int64_t slots = T / block_tokens + 2 * (int64_t)R;
