@@ -520,7 +520,8 @@ qsa_status_t qsa_kv_append_fp8_f16(const void* k, int64_t k_stride_t, int64_t k_
  *              softmax probability, 0 for entries that the row does not see.
  *   workspace  16-byte aligned, qsa_sparse_attention_fp8_workspace_size(T,
  *              Hq, Hkv, width, weights != NULL) bytes; its contents do not
- *              matter before or after.
+ *              matter before or after.  With weights it holds the scores of
+ *              every row, 4 T Hq width bytes.
  * Other arguments, empty rows and errors as qsa_sparse_attention; besides,
  * QSA_ERR_UNSUPPORTED when the cache spans 2^31 - 1 or more multiples of the
  * greatest common divisor of its strides (512 GiB at a divisor of 256), or

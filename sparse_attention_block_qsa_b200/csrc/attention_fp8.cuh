@@ -48,13 +48,13 @@
 //    its own, 2^(s - M) with a second reference: 234 us in place of 210 for 1,024 rows.)
 //
 // Measured on B200 (24 / 2 heads, 2,051 entries a row): 16 requests x 4 rows
-// 25.4 us with the merge (108 MB of distinct rows, 110 MB of DRAM reads; 16.5 us at
-// the copy rate), one row 8.5 us, 1,024 rows 200 us (2.15 GB gathered out of L2: 10.7
-// TB/s).  The last is near what shared memory carries: of about 1,600
+// 26.9 us with the merge (108 MB of distinct rows, 110 MB of DRAM reads; 16.5 us at
+// the copy rate), one row 9.1 us, 1,024 rows 210 us (2.15 GB gathered out of L2: 10.2
+// TB/s).  The last is near what shared memory carries: of about 1,650
 // cycles a tile and SM, 512 write the gathered rows (128 bytes a cycle) and 670
 // feed the MMAs (16 of M128 N32..48 K32, 42 to 45 cycles each alone), so the gather
 // moves as little else through it as it can: 8 lanes copy both halves of a row, so
-// that one shuffle serves two copies (217 us with 16 lanes a row).
+// that one shuffle serves two copies (204 us in place of 217 with 16 lanes a row, then).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -1217,12 +1217,14 @@ static void launch_append(const qsa::kv8::AppendParams& p, int64_t slots, cudaSt
   const int bt = p.block_tokens, threads = APPEND_WARPS * 32;
   const dim3 by_cta((unsigned)slots, (unsigned)p.Hkv, 2);
   const dim3 by_warp((unsigned)((slots + APPEND_WARPS - 1) / APPEND_WARPS), (unsigned)p.Hkv, 2);
-  // A warp per block where it holds the block's rows: 7,680 rows x 4 heads take 33, 16 and 14 us for blocks of 1, 4 and 8
-  // tokens, and 157, 46 and 29 us with a CTA per block.  Blocks of 5 to 8 tokens only where their CTAs would not fit the
-  // GPU at once (6 on an SM): 300 rows x 2 heads take 4.5 us that way and 3.2 us with a CTA each.
+  // A warp per block where it holds the block's rows: 8,000 rows x 4 heads take 26, 14 and 13 us for blocks of 1, 4 and 8
+  // tokens, and 101, 31 and 20 us with a CTA per block; 16 rows x 2 heads take 2.4, 2.8 and 3.2 us, and 2.9, 2.9 and 3.0.
+  // Blocks of 5 to 8 tokens only in numbers: a warp's rows one after the other are slower than a CTA's warps at once
+  // until the CTAs queue.  Warps against CTAs by `slots * Hkv * 2`: 5 tokens 568: 3.7 and 3.2 us, 888: 3.9 and 3.8,
+  // 1,288: 4.2 and 4.6; 8 tokens 356: 4.1 and 3.1, 808: 4.5 and 4.0, 1,208: 5.0 and 4.9, 2,008: 5.6 and 6.5.
   if (bt == 1) append_kernel<F16, 1, 1, false><<<by_warp, threads, 0, s>>>(p);
   else if (bt <= 4) append_kernel<F16, 1, 4, false><<<by_warp, threads, 0, s>>>(p);
-  else if (bt <= 8 && slots * p.Hkv * 2 > 148 * 6) append_kernel<F16, 1, 8, false><<<by_warp, threads, 0, s>>>(p);
+  else if (bt <= 8 && slots * p.Hkv * 2 > 888) append_kernel<F16, 1, 8, false><<<by_warp, threads, 0, s>>>(p);
   else if (bt <= 4 * APPEND_WARPS) append_kernel<F16, APPEND_WARPS, 4, false><<<by_cta, threads, 0, s>>>(p);
   else append_kernel<F16, APPEND_WARPS, 4, true><<<by_cta, threads, 0, s>>>(p);
 }
@@ -1456,9 +1458,14 @@ static qsa_status_t attention_fp8_common(
   if (total > INT32_MAX / 2) return fail(QSA_ERR_UNSUPPORTED, "too many rows for one launch");
   const int HG = p.group <= 8 ? 8 : p.group <= 12 ? 12 : 16;   // query heads the kernel holds
   p.ctas = (int32_t)std::min(total, f16 && HG == 16 ? kAttn8Runs / 2 : kAttn8Runs);
-  // Whole pairs for every run where that makes no run more than 4 tiles longer (24 / 2 heads, 17 tiles a pair: 1 tile
-  // longer 60.6 us against 65.5 with cut pairs and their merge, 4 longer 60.0 and 61.7, 5 longer 60.0 and 60.4); else runs
-  // equal to one tile.
+  // Whole pairs for every run where that makes no run more than 4 tiles longer; else runs equal to one tile, whose cut
+  // pairs a second launch merges.  Whole against cut (24 / 2 heads): 17 tiles a pair, 260 pairs, 2 tiles longer 33.4 us and
+  // 38.9; 300 pairs, 16 longer 50.8 and 38.4; 10 tiles, 260 pairs, 1 longer 22.7 and 29.8; 120 pairs, 5 longer 18.3 and
+  // 18.4; 5 tiles, 120 pairs, 2 longer 12.4 and 14.6, 300 pairs, 4 longer 21.0 and 20.2.  On a GPU that the pairs leave mostly
+  // idle cutting is faster on the device (2 pairs of 3 tiles 9.2 and 8.5, of 5 tiles 11.9 and 8.6), but a call from the host
+  // is not (21.9 us with one launch, 25.1 with two).  With weights, whose second launch is there anyway, cutting is faster
+  // from 2 to 4 tiles on (300 pairs of 3 tiles 24.4 and 22.1, of 5 tiles 30.4 and 26.3; 120 pairs of 5 tiles, 2 longer, 18.3
+  // and 21.8).
   const int64_t all_pairs = T * Hkv, most = (all_pairs + p.ctas - 1) / p.ctas;
   const bool whole = p.tiles == 1 || most * p.tiles - (total + p.ctas - 1) / p.ctas <= 4;
   p.unit = whole ? p.tiles : 1;
@@ -1564,10 +1571,11 @@ qsa_status_t qsa_accumulate_weights(const float* weights, int64_t weights_stride
   return launch_status("weight accumulation kernel");
 }
 
-// Whether one CTA per request sums its pages itself, in one launch: a CTA reads about 50 GB/s, so for tables of 32,768
-// tokens (256 KB) that is 5 us, less than a second launch costs the host (16 requests of 32,000: 16.4 us a call, 20.4 with
-// two).  On the device 16 requests of 102,400 tokens take 19.1 us this way and 9.3 us with two launches; with more
-// requests than SMs the CTAs queue (256 of 40,000: 20.1 and 17.1).
+// Whether one CTA per request sums its pages itself, in one launch.  On the device, one launch against two: 16 requests of
+// 4,000 tokens 6.6 us and 7.6, of 16,000 7.0 and 8.2, of 32,000 10.8 and 10.0 (8.9 and 8.2 in pages of 64 instead of 16);
+// one request of 32,000 10.4 and 8.9; 148 of 16,000 7.7 and 11.0, of 32,000 11.2 and 14.9.  A call from the host saves 4 us
+// more (16.5 and 21).  Longer tables are too much for one CTA, which reads about 50 GB/s (16 requests of 102,400 tokens 19.1 and
+// 9.3), and with more requests than SMs the CTAs queue (256 of 4,000 12.3 and 9.9, of 32,000 20.3 and 19.1).
 static bool evict_in_one(int32_t R, int32_t max_pages, int32_t page_size) {
   return R <= 148 && max_pages <= 4096 && (int64_t)max_pages * page_size <= 32768;
 }
